@@ -68,6 +68,7 @@ typedef int32_t moe_status;
 #define MOE_WFMT_BF16   0   /* bf16 matrices [E, out, in]                       */
 #define MOE_WFMT_Q3G128 1   /* 3-bit codes, groups of 128 along `in`, fp16 scale */
 #define MOE_WFMT_BF16_PAIRS 2 /* row-pair layout (moe_pack_bf16_pairs): gate/up bf16, down fp16 */
+#define MOE_WFMT_FP8_B128 4 /* e4m3 matrices [E, out, in], one fp32 scale per 128 x 128 block   */
 
 #define MOE_MAX_TOPK    32
 #define MOE_MAX_EXPERTS 1024
@@ -88,7 +89,10 @@ const char* moe_version(void);
  * weight format `wfmt`.  One buffer of this size serves both calls (they
  * use it in stream order).  MOE_WFMT_Q3G128 needs T*H*2 + T*(H/128)*4 more
  * bytes (rounded up to 256 each) than MOE_WFMT_BF16: a reordered copy of the
- * thin experts' activation rows and their 128-group sums.  Returns 0 for
+ * thin experts' activation rows and their 128-group sums.  MOE_WFMT_FP8_B128
+ * keeps the activation a in T*k*I + T*k*(I/128)*4 bytes (e4m3 codes, fp32
+ * scales; the others: T*k*I*2) and needs T*H + T*(H/128)*4 more for the codes
+ * and scales of x (each part rounded up to 256).  Returns 0 for
  * arguments that are invalid or unsupported.  Alignment: 256 bytes (any
  * hipMalloc pointer).
  */
@@ -188,7 +192,8 @@ moe_status moe_permute(const int32_t* topk_ids, int T, int E, int k,
  *            as the down projection converts them (below), in the row-pair
  *            layout (moe_pack_bf16_pairs with to_fp16 = 1)
  * s_gate, s_up, s_down   fp16 scales [E, I, H/128] / [E, H, I/128] for
- *            MOE_WFMT_Q3G128 (must be NULL for the bf16 formats).  3-bit group
+ *            MOE_WFMT_Q3G128, fp32 block scales for MOE_WFMT_FP8_B128 (below;
+ *            must be NULL for the bf16 formats).  3-bit group
  *            layout: 13 words per 128 weights; field j of a word at bits
  *            [3j, 3j+3), 10 fields in words 0..11, 8 in word 12; weight =
  *            scale * (field - 4).
@@ -212,11 +217,28 @@ moe_status moe_permute(const int32_t* topk_ids, int T, int E, int k,
  */
 moe_status moe_grouped_ffn(const uint16_t* x, int wfmt,
                            const void* w_gate, const void* w_up, const void* w_down,
-                           const uint16_t* s_gate, const uint16_t* s_up, const uint16_t* s_down,
+                           const void* s_gate, const void* s_up, const void* s_down,
                            const int32_t* expert_offsets, const int32_t* sorted_pair,
                            int T, int E, int k, int H, int I, int fat_threshold,
                            uint16_t* y_sorted, void* workspace, size_t workspace_bytes,
                            void* stream);
+
+/*
+ * MOE_WFMT_FP8_B128: the products in 8-bit floating point.  Weights are e4m3
+ * codes (OCP: 4 exponent, 3 mantissa bits, largest value 448, no infinities),
+ * w_gate and w_up [E, I, H], w_down [E, H, I], with one fp32 scale per
+ * 128 x 128 block: s_gate, s_up [E, I/128, H/128], s_down [E, H/128, I/128];
+ * weight = code * scale (any finite scales; moe_quantize_fp8 with block_rows
+ * = 128 makes them).  The activations are quantised as moe_quantize_fp8 with
+ * block_rows = 1 does: x by moe_ffn_gate_up on its way in, a = silu(g) * u
+ * (fp32) in its epilogue:
+ *     g[n] = sum_b sx[t, b] s_gate[n/128, b] sum_{h in b} xq[t, h] w_gate[n, h]
+ * and likewise u, and y from the codes of a and w_down.  Each 128-column
+ * product accumulates in fp32 and takes both scales before it is added in
+ * fp32.  NaN or infinite values of x or a become the NaN code and make their
+ * rows of y NaN.  x, the weights and y_sorted must be 16-byte aligned, the
+ * scales 4-byte, else MOE_ERR_INVALID_ARG; shapes as for the other formats.
+ */
 
 /*
  * The three steps of moe_grouped_ffn, callable one by one (same arguments,
@@ -259,13 +281,13 @@ moe_status moe_route_permute_plan(const float* logits, int T, int E, int k, int 
  * also writes the reordered activation rows of the short lists into the
  * workspace before its streaming kernel. */
 moe_status moe_ffn_gate_up(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up,
-                           const uint16_t* s_gate, const uint16_t* s_up, const int32_t* sorted_pair,
+                           const void* s_gate, const void* s_up, const int32_t* sorted_pair,
                            int T, int E, int k, int H, int I, int fat_threshold, void* workspace,
                            size_t workspace_bytes, void* stream);
 
 /* moe_ffn_down -- y_sorted = a W_down^T for every planned batch (same
  * fat_threshold rule as moe_ffn_gate_up). */
-moe_status moe_ffn_down(int wfmt, const void* w_down, const uint16_t* s_down, int T, int E, int k, int H, int I,
+moe_status moe_ffn_down(int wfmt, const void* w_down, const void* s_down, int T, int E, int k, int H, int I,
                         int fat_threshold, uint16_t* y_sorted, void* workspace, size_t workspace_bytes,
                         void* stream);
 
@@ -291,8 +313,8 @@ moe_status moe_ffn_down(int wfmt, const void* w_down, const uint16_t* s_down, in
  * safe.
  */
 moe_status moe_grouped_ffn_noalloc(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up,
-                                   const void* w_down, const uint16_t* s_gate, const uint16_t* s_up,
-                                   const uint16_t* s_down, const int32_t* expert_offsets, const int32_t* sorted_pair,
+                                   const void* w_down, const void* s_gate, const void* s_up,
+                                   const void* s_down, const int32_t* expert_offsets, const int32_t* sorted_pair,
                                    int T, int E, int k, int H, int I, int fat_threshold, uint16_t* y_sorted,
                                    void* stream);
 
@@ -329,6 +351,105 @@ moe_status moe_pack_bf16_pairs(const uint16_t* src, uint16_t* dst, int64_t mats,
  */
 moe_status moe_combine(const uint16_t* y_sorted, const float* topk_w, const int32_t* pair_to_sorted,
                        int T, int k, int H, float* out, void* stream);
+
+/*
+ * moe_quantize_fp8 -- e4m3 codes and block scales of bf16 matrices.
+ *
+ * src    bf16 [mats, rows, cols];   codes  uint8, same shape;
+ * scales fp32 [mats, rows / block_rows, cols / 128].
+ * A block is block_rows x 128 values: block_rows = 1 for activations, 128 for
+ * the weights of MOE_WFMT_FP8_B128.  scale = the least power of two s >=
+ * 2^-126 with max|v| <= 448 s over the block's finite values, 1 where that
+ * maximum is 0; code = e4m3 of v / s, nearest even (v / s is exact, so codes
+ * and scales are unique); NaN and infinities become the NaN code 0x7f or
+ * 0xff.  One launch on `stream`.
+ * Errors: NULL pointers, src or codes not 16-byte aligned, scales not 4-byte
+ * aligned, mats, rows or cols < 1 -> MOE_ERR_INVALID_ARG; block_rows other
+ * than 1 and 128, cols not a multiple of 128, rows not a multiple of
+ * block_rows, mats * rows * cols of 2^35 or about that -> MOE_ERR_UNSUPPORTED.
+ * src, codes and scales must not overlap.
+ */
+moe_status moe_quantize_fp8(const uint16_t* src, int64_t mats, int rows, int cols, int block_rows, uint8_t* codes,
+                            float* scales, void* stream);
+
+/* Bytes of workspace of moe_balance_loss for T tokens in `groups` groups and
+ * E experts: about 8 E bytes per 64 tokens of a group, rounded up.  0 for
+ * arguments that are invalid or unsupported.  Alignment: 256 bytes. */
+size_t moe_balance_workspace_size(int T, int E, int groups);
+
+/*
+ * moe_balance_loss -- the router's load-balance loss and per-expert counts.
+ *
+ * The T tokens form `groups` groups of L = T / groups consecutive tokens (1:
+ * the whole batch; the batch size of a padded [batch, L] batch: a loss for
+ * each sequence).  p[t, :] = softmax(logits[t, :]) over all E experts; n_g
+ * the counted tokens of group g, G' the groups with n_g > 0:
+ *   expert_counts[g, e]  int32  (token, slot) pairs of counted tokens with
+ *                               topk_ids = e
+ *   prob_mean[g, e]      fp32   sum_t p[t, e] / n_g (0 for an empty group)
+ *   loss                 fp32   coef / G' * sum_g E / (k n_g)
+ *                                 * sum_e expert_counts[g, e] prob_mean[g, e]
+ *   group_scale[g]       fp32   coef E / (k n_g^2 G'), 0 for an empty group;
+ *                               what moe_route_backward needs of the loss
+ * A uniform router's loss is coef.  No counted token at all: loss 0.
+ * token_mask   uint8 [T] or NULL: tokens with 0 are not counted, and their
+ *              logits and ids are not read (padding may hold anything).
+ * Logits of counted tokens may be -inf (probability 0; all -inf: p = 0); NaN
+ * or +inf make the outputs of their group and the loss NaN.  Ids outside
+ * [0, E) are not counted.  Sums are fp32 in a fixed order, no float atomics:
+ * bit-identical across runs.  Two launches.
+ * Errors: NULL pointers (token_mask aside), T, E, k as moe_route_topk, groups
+ * < 1 or not dividing T, a workspace that is not 256-byte aligned ->
+ * MOE_ERR_INVALID_ARG; a workspace that is missing or too small ->
+ * MOE_ERR_WORKSPACE; over 2^24 blocks of tokens -> MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E,
+                            int k, int groups, float coef, int32_t* expert_counts, float* prob_mean,
+                            float* group_scale, float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_route_backward -- gradient with respect to the router logits, of the
+ * gate weights and of the balance loss, in one pass:
+ *   d_logits[t, e] = p[t, e] (b[t, e] - sum_f p[t, f] b[t, f])
+ *                    + sum_{j: topk_ids[t, j] = e} topk_w[t, j] (d_topk_w[t, j]
+ *                        - sum_i topk_w[t, i] d_topk_w[t, i])
+ *   b[t, e] = d_loss * group_scale[g] * expert_counts[g, e],  g = t / (T / groups)
+ * (the counts and the choice of experts carry no gradient).
+ * expert_counts, group_scale   as written by moe_balance_loss, with the same
+ *            logits, token_mask and groups; d_loss   fp32, one value on the
+ *            device.  All three NULL: no balance term (logits and token_mask
+ *            are then not read).
+ * topk_ids, topk_w   as written by moe_route_topk; d_topk_w   fp32 [T, k], or
+ *            NULL: no gate term.  Masked tokens have no balance term; their
+ *            gate term follows from d_topk_w like any other.  An id outside
+ *            [0, E) is left out of d_logits.
+ * d_logits   fp32 [T, E], every element written; must not overlap an input.
+ * Errors: d_logits NULL, both terms absent, one of the three balance inputs
+ * without the others, balance without logits, d_topk_w without topk_ids or
+ * topk_w, T, E, k, groups as above -> MOE_ERR_INVALID_ARG.
+ */
+moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                              const float* d_topk_w, const int32_t* expert_counts, const float* group_scale,
+                              const float* d_loss, const uint8_t* token_mask, int T, int E, int k, int groups,
+                              float* d_logits, void* stream);
+
+/*
+ * moe_combine_backward -- gradient of moe_combine:
+ *   d_y_sorted[pair_to_sorted[t*k+j], :] = topk_w[t, j] * d_out[t, :]
+ *   d_topk_w[t, j] = sum_h d_out[t, h] * y_sorted[pair_to_sorted[t*k+j], h]
+ * d_out fp32 [T, H]; y_sorted, topk_w, pair_to_sorted as for moe_combine.
+ * d_y_sorted fp16 [T*k, H] (the type of y_sorted, rounded once to nearest; a
+ * product beyond 65504 becomes infinite: scale the loss) or NULL; then topk_w
+ * is not read.  d_topk_w fp32 [T, k] (fp32 sums) or NULL; then y_sorted is
+ * not read.  No atomics: bit-identical across runs.
+ * Errors: d_out or pair_to_sorted NULL, both outputs NULL, an output without
+ * the input it needs, T, k, H as for moe_combine, d_out, y_sorted or
+ * d_y_sorted not 16-byte aligned -> MOE_ERR_INVALID_ARG; H % 8 != 0 ->
+ * MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_combine_backward(const float* d_out, const uint16_t* y_sorted, const float* topk_w,
+                                const int32_t* pair_to_sorted, int T, int k, int H, uint16_t* d_y_sorted,
+                                float* d_topk_w, void* stream);
 
 #ifdef __cplusplus
 }

@@ -313,3 +313,145 @@ def rel_max_err(got, ref) -> float:
     got = np.asarray(got, dtype=np.float64)
     rms = float(np.sqrt(np.mean(ref * ref)))
     return float(np.max(np.abs(got - ref)) / rms) if rms > 0 else float(np.max(np.abs(got - ref)))
+
+
+# ------------------------------------------------- 8-bit blocks (e4m3, scale per 128)
+
+FP8_MAX = 448.0
+FP8_BLOCK = 128
+
+
+def e4m3_to_f64(codes: np.ndarray) -> np.ndarray:
+    """Value of e4m3 codes: 1 sign, 4 exponent (bias 7), 3 mantissa bits; 0x7f and 0xff NaN, no infinities."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    sign = np.where(c & 0x80, -1.0, 1.0)
+    e, m = (c >> 3) & 0xF, (c & 7).astype(np.float64)
+    v = np.where(e > 0, np.ldexp(1.0 + m / 8.0, e - 7), np.ldexp(m / 8.0, -6))
+    return np.where((c & 0x7F) == 0x7F, np.nan, sign * v)
+
+
+def f64_to_e4m3(v: np.ndarray) -> np.ndarray:
+    """Nearest e4m3 code (ties to the even mantissa) of values with |v| <= 448, by search in the table of
+    all non-negative values; non-finite values give the NaN code."""
+    v = np.asarray(v, dtype=np.float64)
+    table = e4m3_to_f64(np.arange(0x7F))                    # 0 .. 448, ascending
+    a = np.where(np.isfinite(v), np.abs(v), 0.0)
+    if np.any(a > FP8_MAX):
+        raise ValueError("value beyond the e4m3 range")
+    hi = np.clip(np.searchsorted(table, a, side="left"), 1, len(table) - 1)
+    lo = hi - 1
+    dl, dh = a - table[lo], table[hi] - a
+    code = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
+    code = np.where(np.signbit(v), code | 0x80, code).astype(np.uint8)
+    return np.where(np.isfinite(v), code, 0x7F).astype(np.uint8)
+
+
+def fp8_block_scale(top: float) -> float:
+    """The least power of two s >= 2^-126 with top <= 448 s; 1 for top = 0."""
+    if top == 0:
+        return 1.0
+    s = 2.0 ** -126
+    while top > FP8_MAX * s:
+        s *= 2.0
+    return s
+
+
+def quantize_fp8(v: np.ndarray, block_rows: int):
+    """(codes uint8 [rows, cols], scales float64 [rows / block_rows, cols / 128]) of one matrix of values."""
+    rows, cols = v.shape
+    codes = np.zeros((rows, cols), dtype=np.uint8)
+    scales = np.ones((rows // block_rows, cols // FP8_BLOCK))
+    for i in range(rows // block_rows):
+        for j in range(cols // FP8_BLOCK):
+            r = slice(i * block_rows, (i + 1) * block_rows)
+            c = slice(j * FP8_BLOCK, (j + 1) * FP8_BLOCK)
+            b = v[r, c]
+            ok = np.isfinite(b)
+            scales[i, j] = fp8_block_scale(float(np.max(np.abs(b[ok]))) if ok.any() else 0.0)
+            codes[r, c] = f64_to_e4m3(b / scales[i, j])
+    return codes, scales
+
+
+def fp8_values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """Values of a matrix of e4m3 codes [rows, cols] with scales [rows / block_rows, cols / 128]."""
+    block_rows = codes.shape[0] // scales.shape[0]
+    return e4m3_to_f64(codes) * np.repeat(np.repeat(np.asarray(scales, dtype=np.float64), block_rows, 0), FP8_BLOCK, 1)
+
+
+def fp8_expert_ffn(xq: np.ndarray, wg: np.ndarray, wu: np.ndarray, wd: np.ndarray):
+    """(y, a, aq) of one expert: xq the quantised values of its rows, the weights as values; aq the values of
+    the quantised activation a."""
+    a = silu(xq @ wg.T) * (xq @ wu.T)
+    aq = fp8_values(*quantize_fp8(a, 1)) if len(a) else a
+    return aq @ wd.T, a, aq
+
+
+# ------------------------------------------------ balance loss and the router's gradient
+
+def balance_loss(logits, ids, groups: int, coef: float, mask=None) -> dict:
+    """counts [G, E], prob [G, E], loss and group_scale [G]: token by token, group by group."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    k = ids.shape[1]
+    L = T // groups
+    counts = np.zeros((groups, E), dtype=np.int64)
+    prob = np.zeros((groups, E))
+    n = np.zeros(groups, dtype=np.int64)
+    for t in range(T):
+        if mask is not None and not mask[t]:
+            continue
+        g = t // L
+        n[g] += 1
+        for e in ids[t]:
+            if 0 <= e < E:
+                counts[g, e] += 1
+        prob[g] += softmax_row(logits[t])
+    live = int(np.count_nonzero(n))
+    scale = np.zeros(groups)
+    loss = 0.0
+    for g in range(groups):
+        if n[g]:
+            prob[g] /= n[g]
+            loss += coef / live * E / (k * n[g]) * float(counts[g] @ prob[g])
+            scale[g] = coef * E / (k * float(n[g]) ** 2 * live)
+    return {"counts": counts, "prob": prob, "loss": loss, "group_scale": scale}
+
+
+def softmax_row(l: np.ndarray) -> np.ndarray:
+    """softmax of one row of logits; all zeros where every logit is -inf."""
+    top = np.max(l)
+    if top == -np.inf:
+        return np.zeros_like(l)
+    e = np.exp(l - top)
+    return e / e.sum()
+
+
+def route_backward(logits, ids, w, d_w=None, balance=None, d_loss: float = 0.0, mask=None) -> np.ndarray:
+    """d_logits [T, E] from the gate weights' gradient d_w [T, k] and the balance loss (``balance`` as
+    returned by balance_loss)."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    d = np.zeros((T, E))
+    for t in range(T):
+        if balance is not None and (mask is None or mask[t]):
+            g = t // (T // len(balance["group_scale"]))
+            p = softmax_row(logits[t])
+            b = d_loss * balance["group_scale"][g] * balance["counts"][g]
+            d[t] += p * (b - p @ b)
+        if d_w is not None:
+            wt, dt = np.asarray(w[t], dtype=np.float64), np.asarray(d_w[t], dtype=np.float64)
+            for j, e in enumerate(ids[t]):
+                d[t, e] += wt[j] * (dt[j] - wt @ dt)
+    return d
+
+
+def combine_backward(d_out, Y, w, pair_to_sorted, k: int):
+    """(d_Y [T*k, H], d_w [T, k]) of out[t] = sum_j w[t, j] Y[pair_to_sorted[t k + j]]."""
+    T, H = d_out.shape
+    d_Y, d_w = np.zeros((T * k, H)), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            i = pair_to_sorted[t * k + j]
+            d_Y[i] = float(w[t, j]) * d_out[t]
+            d_w[t, j] = d_out[t] @ Y[i]
+    return d_Y, d_w

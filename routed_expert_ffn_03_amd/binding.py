@@ -19,12 +19,15 @@ MOE_ERR_HIP = 4
 MOE_WFMT_BF16 = 0
 MOE_WFMT_Q3G128 = 1
 MOE_WFMT_BF16_PAIRS = 2
+MOE_WFMT_FP8_B128 = 4
 
 DEFAULT_FAT_THRESHOLD = 32
 
 EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route_topk", "moe_router_topk",
            "moe_permute", "moe_grouped_ffn", "moe_ffn_plan", "moe_ffn_gate_up", "moe_ffn_down",
-           "moe_combine", "moe_grouped_ffn_noalloc", "moe_route_permute_plan", "moe_pack_bf16_pairs")
+           "moe_combine", "moe_grouped_ffn_noalloc", "moe_route_permute_plan", "moe_pack_bf16_pairs",
+           "moe_quantize_fp8", "moe_balance_workspace_size", "moe_balance_loss", "moe_route_backward",
+           "moe_combine_backward")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -75,6 +78,16 @@ def lib() -> ctypes.CDLL:
         L.moe_combine.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_pack_bf16_pairs.restype = i32
         L.moe_pack_bf16_pairs.argtypes = [vp, vp, ctypes.c_int64, i32, i32, i32, vp]
+        L.moe_quantize_fp8.restype = i32
+        L.moe_quantize_fp8.argtypes = [vp, ctypes.c_int64, i32, i32, i32, vp, vp, vp]
+        L.moe_balance_workspace_size.restype = sz
+        L.moe_balance_workspace_size.argtypes = [i32] * 3
+        L.moe_balance_loss.restype = i32
+        L.moe_balance_loss.argtypes = [vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_route_backward.restype = i32
+        L.moe_route_backward.argtypes = [vp] * 8 + [i32] * 4 + [vp, vp]
+        L.moe_combine_backward.restype = i32
+        L.moe_combine_backward.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -101,6 +114,46 @@ def _check(status: int, what: str):
 def _dev(t: torch.Tensor, dtype, name: str):
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor on the GPU")
+
+
+def _here(**tensors):
+    """Every given tensor lies on the current device, the one the launch and the default stream are on."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _shaped(t, dtype, name: str, shape):
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _codes(t, name: str, shape):
+    """e4m3 codes: uint8 or float8_e4m3fn."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in (torch.uint8, torch.float8_e4m3fn)
+            and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous uint8 or float8_e4m3fn tensor on the GPU")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _fp8_experts(E, H, I, gate_up=None, down=None):
+    """Types and shapes of e4m3 expert weights and their fp32 scales per 128 x 128 block."""
+    if H % 128 or I % 128:
+        raise ValueError(f"e4m3 experts: H = {H} and I = {I} must be multiples of 128")
+    if gate_up is not None:
+        w_gate, w_up, s_gate, s_up = gate_up
+        for w, sc, n in ((w_gate, s_gate, "gate"), (w_up, s_up, "up")):
+            _codes(w, f"w_{n}", (E, I, H))
+            _shaped(sc, torch.float32, f"s_{n}", (E, I // 128, H // 128))
+        _here(w_gate=w_gate, w_up=w_up, s_gate=s_gate, s_up=s_up)
+    if down is not None:
+        w_down, s_down = down
+        _codes(w_down, "w_down", (E, H, I))
+        _shaped(s_down, torch.float32, "s_down", (E, H // 128, I // 128))
+        _here(w_down=w_down, s_down=s_down)
 
 
 def moe_workspace_size(T: int, E: int, k: int, H: int, I: int, wfmt: int = MOE_WFMT_BF16) -> int:
@@ -164,7 +217,8 @@ def moe_grouped_ffn(x, w_gate, w_up, w_down, expert_offsets, sorted_pair, k, y_s
                     s_gate=None, s_up=None, s_down=None, fat_threshold=DEFAULT_FAT_THRESHOLD,
                     wfmt=MOE_WFMT_BF16, stream=None):
     """x, weights and y_sorted hold bf16/fp16 bit patterns (torch.bfloat16 /
-    torch.float16 / int16 tensors are all accepted; 3-bit words are int32)."""
+    torch.float16 / int16 tensors are all accepted; 3-bit words are int32;
+    e4m3 codes are uint8 or float8_e4m3fn with fp32 scales per 128 x 128 block)."""
     T, H = x.shape
     E = expert_offsets.numel() - 1
     I = w_gate.shape[1]          # [E, I, H] bf16 or [E, I, H/128, 13] 3-bit words
@@ -176,6 +230,8 @@ def moe_grouped_ffn(x, w_gate, w_up, w_down, expert_offsets, sorted_pair, k, y_s
         raise ValueError("x and y_sorted must have 16-bit elements")
     if tuple(y_sorted.shape) != (T * k, H):
         raise ValueError(f"y_sorted: shape {tuple(y_sorted.shape)} != {(T * k, H)}")
+    if wfmt == MOE_WFMT_FP8_B128:
+        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down))
     _check(lib().moe_grouped_ffn(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate),
                                  _ptr(s_up), _ptr(s_down), _ptr(expert_offsets), _ptr(sorted_pair), T, E, k, H, I,
                                  fat_threshold, _ptr(y_sorted), _ptr(workspace), workspace.numel(),
@@ -219,6 +275,8 @@ def moe_grouped_ffn_noalloc(x, w_gate, w_up, w_down, expert_offsets, sorted_pair
         raise ValueError("x and y_sorted must have 16-bit elements")
     if tuple(y_sorted.shape) != (T * k, H):
         raise ValueError(f"y_sorted: shape {tuple(y_sorted.shape)} != {(T * k, H)}")
+    if wfmt == MOE_WFMT_FP8_B128:
+        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down))
     _check(lib().moe_grouped_ffn_noalloc(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate),
                                          _ptr(s_up), _ptr(s_down), _ptr(expert_offsets), _ptr(sorted_pair), T, E,
                                          k, H, I, fat_threshold, _ptr(y_sorted), _stream(stream)),
@@ -238,6 +296,8 @@ def moe_ffn_gate_up(x, w_gate, w_up, sorted_pair, E, k, workspace, s_gate=None, 
                     fat_threshold=DEFAULT_FAT_THRESHOLD, wfmt=MOE_WFMT_BF16, stream=None):
     T, H = x.shape
     I = w_gate.shape[1]
+    if wfmt == MOE_WFMT_FP8_B128:
+        _fp8_experts(E, H, I, gate_up=(w_gate, w_up, s_gate, s_up))
     _check(lib().moe_ffn_gate_up(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(s_gate), _ptr(s_up),
                                  _ptr(sorted_pair), T, E, k, H, I, fat_threshold, _ptr(workspace),
                                  workspace.numel(), _stream(stream)), "moe_ffn_gate_up")
@@ -246,6 +306,8 @@ def moe_ffn_gate_up(x, w_gate, w_up, sorted_pair, E, k, workspace, s_gate=None, 
 def moe_ffn_down(w_down, T, E, k, I, y_sorted, workspace, s_down=None, fat_threshold=DEFAULT_FAT_THRESHOLD,
                  wfmt=MOE_WFMT_BF16, stream=None):
     H = y_sorted.shape[1]
+    if wfmt == MOE_WFMT_FP8_B128:
+        _fp8_experts(E, H, I, down=(w_down, s_down))
     _check(lib().moe_ffn_down(wfmt, _ptr(w_down), _ptr(s_down), T, E, k, H, I, fat_threshold, _ptr(y_sorted),
                               _ptr(workspace), workspace.numel(), _stream(stream)), "moe_ffn_down")
 
@@ -275,3 +337,110 @@ def moe_pack_bf16_pairs(src, dst, to_fp16=False, stream=None):
     mats = src.numel() // (rows * cols) if rows * cols else 0
     _check(lib().moe_pack_bf16_pairs(_ptr(src), _ptr(dst), mats, rows, cols, int(bool(to_fp16)), _stream(stream)),
            "moe_pack_bf16_pairs")
+
+
+def moe_quantize_fp8(src, codes, scales, block_rows=1, stream=None):
+    """e4m3 ``codes`` (uint8 or float8_e4m3fn, the shape of ``src``) and fp32 ``scales``
+    [..., rows / block_rows, cols / 128] of bf16 ``src`` [..., rows, cols]; ``block_rows`` 1 for
+    activations, 128 for the weights of ``MOE_WFMT_FP8_B128``."""
+    if not (isinstance(src, torch.Tensor) and src.is_cuda and src.dtype in (torch.bfloat16, torch.int16)
+            and src.is_contiguous()):
+        raise ValueError("src: expected a contiguous bfloat16 (or int16 bit pattern) tensor on the GPU")
+    if src.dim() < 2 or src.numel() == 0:
+        raise ValueError(f"src: shape {tuple(src.shape)}: [..., rows, cols] with at least one value expected")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows {block_rows}: 1 or 128")
+    rows, cols = int(src.shape[-2]), int(src.shape[-1])
+    if cols % 128 or rows % block_rows:
+        raise ValueError(f"src: {rows} x {cols} is not a whole number of {block_rows} x 128 blocks")
+    _codes(codes, "codes", src.shape)
+    _shaped(scales, torch.float32, "scales", (*src.shape[:-2], rows // block_rows, cols // 128))
+    _here(src=src, codes=codes, scales=scales)
+    _check(lib().moe_quantize_fp8(_ptr(src), src.numel() // (rows * cols), rows, cols, block_rows, _ptr(codes),
+                                  _ptr(scales), _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_balance_workspace_size(T: int, E: int, groups: int = 1) -> int:
+    return int(lib().moe_balance_workspace_size(T, E, groups))
+
+
+def _token_mask(mask, T):
+    if mask is not None:
+        if not (isinstance(mask, torch.Tensor) and mask.is_cuda and mask.is_contiguous()
+                and mask.dtype in (torch.uint8, torch.bool) and tuple(mask.shape) == (T,)):
+            raise ValueError(f"token_mask: expected a contiguous uint8 or bool tensor [{T}] on the GPU")
+
+
+def moe_balance_loss(logits, topk_ids, expert_counts, prob_mean, group_scale, loss, workspace, token_mask=None,
+                     coef=1.0, stream=None):
+    """The balance loss and per-expert counts of ``logits`` [T, E] routed to ``topk_ids`` [T, k];
+    ``expert_counts`` (int32) and ``prob_mean`` [G, E] fix the number of groups G, ``group_scale``
+    [G] goes to ``moe_route_backward``; ``loss`` [1]; masked tokens (0) are not counted."""
+    _dev(logits, torch.float32, "logits")
+    T, E = logits.shape
+    G = expert_counts.shape[0]
+    _dev(topk_ids, torch.int32, "topk_ids")
+    k = topk_ids.shape[-1]
+    _shaped(topk_ids, torch.int32, "topk_ids", (T, k))
+    _shaped(expert_counts, torch.int32, "expert_counts", (G, E))
+    _shaped(prob_mean, torch.float32, "prob_mean", (G, E))
+    _shaped(group_scale, torch.float32, "group_scale", (G,))
+    _shaped(loss, torch.float32, "loss", (1,))
+    _token_mask(token_mask, T)
+    _dev(workspace, torch.uint8, "workspace")
+    _here(logits=logits, topk_ids=topk_ids, expert_counts=expert_counts, prob_mean=prob_mean,
+          group_scale=group_scale, loss=loss, workspace=workspace, token_mask=token_mask)
+    _check(lib().moe_balance_loss(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k, G, float(coef),
+                                  _ptr(expert_counts), _ptr(prob_mean), _ptr(group_scale), _ptr(loss),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(logits, topk_ids, topk_w, d_logits, d_topk_w=None, expert_counts=None, group_scale=None,
+                       d_loss=None, token_mask=None, stream=None):
+    """``d_logits`` [T, E] of the gate weights (``d_topk_w`` [T, k], or none) and of the balance loss
+    (``expert_counts`` [G, E] and ``group_scale`` [G] from ``moe_balance_loss``, ``d_loss`` [1]; or none
+    of the three)."""
+    _dev(d_logits, torch.float32, "d_logits")
+    T, E = d_logits.shape
+    _dev(topk_ids, torch.int32, "topk_ids")
+    k = topk_ids.shape[-1]
+    G = 1
+    _shaped(logits, torch.float32, "logits", (T, E))
+    _shaped(topk_ids, torch.int32, "topk_ids", (T, k))
+    _shaped(topk_w, torch.float32, "topk_w", (T, k))
+    if d_topk_w is not None:
+        _shaped(d_topk_w, torch.float32, "d_topk_w", (T, k))
+    if expert_counts is not None:
+        G = expert_counts.shape[0]
+        _shaped(expert_counts, torch.int32, "expert_counts", (G, E))
+    if group_scale is not None:
+        _shaped(group_scale, torch.float32, "group_scale", (G,))
+    if d_loss is not None:
+        _shaped(d_loss, torch.float32, "d_loss", (1,))
+    _token_mask(token_mask, T)
+    _here(logits=logits, topk_ids=topk_ids, topk_w=topk_w, d_logits=d_logits, d_topk_w=d_topk_w,
+          expert_counts=expert_counts, group_scale=group_scale, d_loss=d_loss, token_mask=token_mask)
+    _check(lib().moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w), _ptr(expert_counts),
+                                    _ptr(group_scale), _ptr(d_loss), _ptr(token_mask), T, E, k, G, _ptr(d_logits),
+                                    _stream(stream)), "moe_route_backward")
+
+
+def moe_combine_backward(d_out, y_sorted, topk_w, pair_to_sorted, d_y_sorted=None, d_topk_w=None, stream=None):
+    """Gradient of ``moe_combine``: ``d_y_sorted`` (fp16, the shape of ``y_sorted``) and ``d_topk_w``
+    (fp32 [T, k]), either may be None."""
+    _dev(d_out, torch.float32, "d_out")
+    T, H = d_out.shape
+    _dev(topk_w, torch.float32, "topk_w")
+    k = topk_w.shape[-1]
+    _shaped(topk_w, torch.float32, "topk_w", (T, k))
+    _shaped(pair_to_sorted, torch.int32, "pair_to_sorted", (T * k,))
+    for t, name in ((y_sorted, "y_sorted"), (d_y_sorted, "d_y_sorted")):
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype in (torch.float16, torch.int16)
+                                  and tuple(t.shape) == (T * k, H)):
+            raise ValueError(f"{name}: expected a contiguous fp16 tensor {(T * k, H)} on the GPU")
+    if d_topk_w is not None:
+        _shaped(d_topk_w, torch.float32, "d_topk_w", (T, k))
+    _here(d_out=d_out, y_sorted=y_sorted, topk_w=topk_w, pair_to_sorted=pair_to_sorted, d_y_sorted=d_y_sorted,
+          d_topk_w=d_topk_w)
+    _check(lib().moe_combine_backward(_ptr(d_out), _ptr(y_sorted), _ptr(topk_w), _ptr(pair_to_sorted), T, k, H,
+                                      _ptr(d_y_sorted), _ptr(d_topk_w), _stream(stream)), "moe_combine_backward")

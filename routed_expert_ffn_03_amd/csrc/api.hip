@@ -5,6 +5,7 @@
 // section "The prestage, per decode step", point 4.
 #include "../../include/moe_mi355x.h"
 #include "ffn_shared.h"
+#include "fp8.h"
 #include "kernels.h"
 
 #include <mutex>
@@ -59,7 +60,8 @@ bool ffn_shape_ok(int T, int k, int H, int I) {
 moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool wfmt_known(int wfmt) {
-    return wfmt == MOE_WFMT_BF16 || wfmt == MOE_WFMT_Q3G128 || wfmt == MOE_WFMT_BF16_PAIRS;
+    return wfmt == MOE_WFMT_BF16 || wfmt == MOE_WFMT_Q3G128 || wfmt == MOE_WFMT_BF16_PAIRS ||
+           wfmt == MOE_WFMT_FP8_B128;
 }
 
 // Shape rules of a format beyond ffn_shape_ok: the row-pair layout is read
@@ -71,9 +73,18 @@ bool wfmt_shape_ok(int wfmt, int T, int k, int H, int I) {
     return moe::stream_fits(1, T, k, H, I) && moe::stream_fits(2, T, k, H, I);
 }
 
-// Scales come with the 3-bit format and only with it.
+// Scales come with the 3-bit and e4m3 formats and only with them.
 bool scales_ok(int wfmt, const void* a, const void* b) {
-    return wfmt == MOE_WFMT_Q3G128 ? (a && b) : (!a && !b);
+    return wfmt == MOE_WFMT_Q3G128 || wfmt == MOE_WFMT_FP8_B128 ? (a && b) : (!a && !b);
+}
+
+// The e4m3 kernels move 16 bytes at a time from the first byte of x, of a
+// weight matrix and of y, and read whole fp32 scales.
+bool fp8_aligned(int wfmt, const void* a, const void* b, const void* c, const void* s0, const void* s1,
+                 const void* s2) {
+    if (wfmt != MOE_WFMT_FP8_B128) return true;
+    return (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0 &&
+           (((uintptr_t)s0 | (uintptr_t)s1 | (uintptr_t)s2) & 3) == 0;
 }
 
 }  // namespace
@@ -158,12 +169,13 @@ moe_status moe_ffn_plan(const int32_t* expert_offsets, int T, int E, int k, int 
 }
 
 moe_status moe_ffn_gate_up(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up,
-                           const uint16_t* s_gate, const uint16_t* s_up, const int32_t* sorted_pair,
+                           const void* s_gate, const void* s_up, const int32_t* sorted_pair,
                            int T, int E, int k, int H, int I, int fat_threshold, void* workspace,
                            size_t workspace_bytes, void* stream) {
     if (!x || !w_gate || !w_up || !sorted_pair || fat_threshold < 1) return MOE_ERR_INVALID_ARG;
     if (wfmt_known(wfmt) && !scales_ok(wfmt, s_gate, s_up))
         return MOE_ERR_INVALID_ARG;
+    if (!fp8_aligned(wfmt, x, w_gate, w_up, s_gate, s_up, nullptr)) return MOE_ERR_INVALID_ARG;
     moe::FfnLaunch a;
     moe_status st = ffn_prepare(a, wfmt, T, E, k, H, I, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
@@ -175,12 +187,13 @@ moe_status moe_ffn_gate_up(const uint16_t* x, int wfmt, const void* w_gate, cons
     return hip_status(moe::launch_ffn_phase(a, 1, reinterpret_cast<hipStream_t>(stream)));
 }
 
-moe_status moe_ffn_down(int wfmt, const void* w_down, const uint16_t* s_down, int T, int E, int k, int H, int I,
+moe_status moe_ffn_down(int wfmt, const void* w_down, const void* s_down, int T, int E, int k, int H, int I,
                         int fat_threshold, uint16_t* y_sorted, void* workspace, size_t workspace_bytes,
                         void* stream) {
     if (!w_down || !y_sorted || fat_threshold < 1) return MOE_ERR_INVALID_ARG;
     if (wfmt_known(wfmt) && !scales_ok(wfmt, s_down, s_down))
         return MOE_ERR_INVALID_ARG;
+    if (!fp8_aligned(wfmt, w_down, y_sorted, nullptr, s_down, nullptr, nullptr)) return MOE_ERR_INVALID_ARG;
     moe::FfnLaunch a;
     moe_status st = ffn_prepare(a, wfmt, T, E, k, H, I, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
@@ -192,7 +205,7 @@ moe_status moe_ffn_down(int wfmt, const void* w_down, const uint16_t* s_down, in
 }
 
 moe_status moe_grouped_ffn(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up, const void* w_down,
-                           const uint16_t* s_gate, const uint16_t* s_up, const uint16_t* s_down,
+                           const void* s_gate, const void* s_up, const void* s_down,
                            const int32_t* expert_offsets, const int32_t* sorted_pair, int T, int E, int k, int H,
                            int I, int fat_threshold, uint16_t* y_sorted, void* workspace, size_t workspace_bytes,
                            void* stream) {
@@ -202,6 +215,9 @@ moe_status moe_grouped_ffn(const uint16_t* x, int wfmt, const void* w_gate, cons
     if (wfmt_known(wfmt)) {
         if (!scales_ok(wfmt, s_gate, s_up) || !scales_ok(wfmt, s_down, s_down)) return MOE_ERR_INVALID_ARG;
     }
+    if (!fp8_aligned(wfmt, x, w_gate, w_up, s_gate, s_up, s_down) ||
+        !fp8_aligned(wfmt, w_down, y_sorted, nullptr, nullptr, nullptr, nullptr))
+        return MOE_ERR_INVALID_ARG;
     moe::FfnLaunch a;
     moe_status st = ffn_prepare(a, wfmt, T, E, k, H, I, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
@@ -245,8 +261,8 @@ moe_status moe_route_permute_plan(const float* logits, int T, int E, int k, int 
 }
 
 moe_status moe_grouped_ffn_noalloc(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up,
-                                   const void* w_down, const uint16_t* s_gate, const uint16_t* s_up,
-                                   const uint16_t* s_down, const int32_t* expert_offsets, const int32_t* sorted_pair,
+                                   const void* w_down, const void* s_gate, const void* s_up,
+                                   const void* s_down, const int32_t* expert_offsets, const int32_t* sorted_pair,
                                    int T, int E, int k, int H, int I, int fat_threshold, uint16_t* y_sorted,
                                    void* stream) {
     if (!x || !w_gate || !w_up || !w_down || !expert_offsets || !sorted_pair || !y_sorted)
@@ -254,6 +270,9 @@ moe_status moe_grouped_ffn_noalloc(const uint16_t* x, int wfmt, const void* w_ga
     if (fat_threshold < 1 || bad_tek(T, E, k) || H < 1 || I < 1) return MOE_ERR_INVALID_ARG;
     if (!wfmt_known(wfmt)) return MOE_ERR_UNSUPPORTED;
     if (!scales_ok(wfmt, s_gate, s_up) || !scales_ok(wfmt, s_down, s_down)) return MOE_ERR_INVALID_ARG;
+    if (!fp8_aligned(wfmt, x, w_gate, w_up, s_gate, s_up, s_down) ||
+        !fp8_aligned(wfmt, w_down, y_sorted, nullptr, nullptr, nullptr, nullptr))
+        return MOE_ERR_INVALID_ARG;
     if (!ffn_shape_ok(T, k, H, I) || !wfmt_shape_ok(wfmt, T, k, H, I)) return MOE_ERR_UNSUPPORTED;
     if (moe::ffn_ws_bytes(T, E, k, H, I, wfmt) > MOE_NOALLOC_SCRATCH_BYTES) return MOE_ERR_WORKSPACE;
     void* ws = nullptr;
@@ -291,6 +310,70 @@ moe_status moe_pack_bf16_pairs(const uint16_t* src, uint16_t* dst, int64_t mats,
     const uintptr_t s0 = (uintptr_t)src, d0 = (uintptr_t)dst;
     if (s0 < d0 + bytes && d0 < s0 + bytes) return MOE_ERR_INVALID_ARG;     // overlapping buffers
     return hip_status(moe::launch_pack_pairs(src, dst, mats, rows, cols, to_fp16, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_quantize_fp8(const uint16_t* src, int64_t mats, int rows, int cols, int block_rows, uint8_t* codes,
+                            float* scales, void* stream) {
+    if (!src || !codes || !scales || mats < 1 || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)src | (uintptr_t)codes) & 15 || (uintptr_t)scales & 3) return MOE_ERR_INVALID_ARG;
+    if (block_rows != 1 && block_rows != 128) return MOE_ERR_UNSUPPORTED;
+    if (cols % 128 || rows % block_rows) return MOE_ERR_UNSUPPORTED;
+    // 8 (rows) or 64 (blocks) values per thread, fewer than 2^32 threads
+    const unsigned long long per = (unsigned long long)rows * (unsigned long long)cols;
+    if ((unsigned long long)mats >= (1ull << 35) / per) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_quantize_fp8(src, mats, rows, cols, block_rows, codes, scales,
+                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+// Shared checks of the balance loss and the router's gradient.
+static moe_status balance_shape(int T, int E, int k, int groups) {
+    if (bad_tek(T, E, k) || groups < 1 || groups > T || T % groups) return MOE_ERR_INVALID_ARG;
+    return moe::balance_shape_ok(T, E, groups) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+size_t moe_balance_workspace_size(int T, int E, int groups) {
+    return balance_shape(T, E, 1, groups) == MOE_OK ? moe::balance_ws_bytes(T, E, groups) : 0;
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E,
+                            int k, int groups, float coef, int32_t* expert_counts, float* prob_mean,
+                            float* group_scale, float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!logits || !topk_ids || !expert_counts || !prob_mean || !group_scale || !loss) return MOE_ERR_INVALID_ARG;
+    const moe_status st = balance_shape(T, E, k, groups);
+    if (st != MOE_OK) return st;
+    if (!workspace || workspace_bytes < moe::balance_ws_bytes(T, E, groups)) return MOE_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 255) return MOE_ERR_INVALID_ARG;
+    return hip_status(moe::launch_balance_loss(logits, topk_ids, token_mask, T, E, k, groups, coef, expert_counts,
+                                               prob_mean, group_scale, loss, workspace,
+                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                              const float* d_topk_w, const int32_t* expert_counts, const float* group_scale,
+                              const float* d_loss, const uint8_t* token_mask, int T, int E, int k, int groups,
+                              float* d_logits, void* stream) {
+    const bool balance = expert_counts && group_scale && d_loss;
+    if (!d_logits || (!d_topk_w && !balance)) return MOE_ERR_INVALID_ARG;
+    if (!balance && (expert_counts || group_scale || d_loss)) return MOE_ERR_INVALID_ARG;
+    if (balance && !logits) return MOE_ERR_INVALID_ARG;
+    if (d_topk_w && (!topk_ids || !topk_w)) return MOE_ERR_INVALID_ARG;
+    if (bad_tek(T, E, k) || groups < 1 || groups > T || T % groups) return MOE_ERR_INVALID_ARG;
+    return hip_status(moe::launch_route_backward(logits, topk_ids, topk_w, d_topk_w, expert_counts, group_scale,
+                                                 d_loss, token_mask, T, E, k, groups, d_logits,
+                                                 reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_combine_backward(const float* d_out, const uint16_t* y_sorted, const float* topk_w,
+                                const int32_t* pair_to_sorted, int T, int k, int H, uint16_t* d_y_sorted,
+                                float* d_topk_w, void* stream) {
+    if (!d_out || !pair_to_sorted || (!d_y_sorted && !d_topk_w)) return MOE_ERR_INVALID_ARG;
+    if ((d_y_sorted && !topk_w) || (d_topk_w && !y_sorted)) return MOE_ERR_INVALID_ARG;
+    if (T < 1 || k < 1 || k > moe::MAX_TOPK || H < 1 || (long long)T * k >= (1LL << 31))
+        return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)d_out | (uintptr_t)y_sorted | (uintptr_t)d_y_sorted) & 15) return MOE_ERR_INVALID_ARG;
+    if (H % 8) return MOE_ERR_UNSUPPORTED;
+    return hip_status(moe::launch_combine_backward(d_out, y_sorted, topk_w, pair_to_sorted, T, k, H, d_y_sorted,
+                                                   d_topk_w, reinterpret_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_combine(const uint16_t* y_sorted, const float* topk_w, const int32_t* pair_to_sorted, int T, int k,

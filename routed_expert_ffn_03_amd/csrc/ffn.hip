@@ -46,6 +46,7 @@
 // (pair-slot path).
 #include "common.h"
 #include "ffn_shared.h"
+#include "fp8.h"
 #include "kernels.h"
 #include "lds_dma.h"
 
@@ -1212,7 +1213,7 @@ void ffn_thin_q3_kernel(FfnArgs a) {
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct FfnLayout {
-    size_t hdr, fat, thin, act, xq, xs, total;
+    size_t hdr, fat, thin, act, as, xq, xs, total;
     size_t max_fat, max_thin;
 };
 
@@ -1226,7 +1227,15 @@ FfnLayout ffn_layout(int T, int E, int k, int H, int I, int wfmt) {
     L.fat = align256(sizeof(FfnHeader));
     L.thin = L.fat + align256(L.max_fat * sizeof(MTile));
     L.act = L.thin + align256(L.max_thin * sizeof(MTile));
-    L.xq = L.act + align256(P * (size_t)I * sizeof(uint16_t));
+    if (wfmt == 4) {
+        // e4m3 weights: codes and scales of a and of x
+        L.as = L.act + align256(P * (size_t)I);
+        L.xq = L.as + align256(P * (size_t)(I / 128) * sizeof(float));
+        L.xs = L.xq + align256((size_t)T * H);
+        L.total = L.xs + align256((size_t)T * (H / 128) * sizeof(float));
+        return L;
+    }
+    L.xq = L.as = L.act + align256(P * (size_t)I * sizeof(uint16_t));
     // 3-bit weights: reordered x rows and group sums for the thin gate/up path
     const size_t xq_bytes = wfmt == 1 ? align256((size_t)T * H * sizeof(uint16_t)) : 0;
     L.xs = L.xq + xq_bytes;
@@ -1310,7 +1319,9 @@ FfnArgs make_args(const FfnLaunch& a) {
     FfnArgs fa;
     fa.x = a.x;
     fa.wg = a.wg; fa.wu = a.wu; fa.wd = a.wd;
-    fa.sg = a.sg; fa.su = a.su; fa.sd = a.sd;
+    fa.sg = reinterpret_cast<const uint16_t*>(a.sg);
+    fa.su = reinterpret_cast<const uint16_t*>(a.su);
+    fa.sd = reinterpret_cast<const uint16_t*>(a.sd);
     fa.sorted_pair = a.sorted_pair;
     fa.T = a.T; fa.k = a.k; fa.H = a.H; fa.I = a.I; fa.E = a.E;
     fa.pairs = a.wfmt == 2;
@@ -1322,6 +1333,30 @@ FfnArgs make_args(const FfnLaunch& a) {
     fa.fat = reinterpret_cast<MTile*>(ws + L.fat);
     fa.thin = reinterpret_cast<MTile*>(ws + L.thin);
     return fa;
+}
+
+Fp8Args make_fp8_args(const FfnLaunch& a) {
+    const FfnLayout L = ffn_layout(a.T, a.E, a.k, a.H, a.I, a.wfmt);
+    char* ws = reinterpret_cast<char*>(a.ws);
+    Fp8Args f;
+    f.x = a.x;
+    f.wg = reinterpret_cast<const uint8_t*>(a.wg);
+    f.wu = reinterpret_cast<const uint8_t*>(a.wu);
+    f.wd = reinterpret_cast<const uint8_t*>(a.wd);
+    f.sg = reinterpret_cast<const float*>(a.sg);
+    f.su = reinterpret_cast<const float*>(a.su);
+    f.sd = reinterpret_cast<const float*>(a.sd);
+    f.sorted_pair = a.sorted_pair;
+    f.T = a.T; f.k = a.k; f.H = a.H; f.I = a.I; f.E = a.E;
+    f.xq = reinterpret_cast<uint8_t*>(ws + L.xq);
+    f.xs = reinterpret_cast<float*>(ws + L.xs);
+    f.act = reinterpret_cast<uint8_t*>(ws + L.act);
+    f.as = reinterpret_cast<float*>(ws + L.as);
+    f.y = a.y;
+    f.hdr = reinterpret_cast<const FfnHeader*>(ws + L.hdr);
+    f.fat = reinterpret_cast<const MTile*>(ws + L.fat);
+    f.thin = reinterpret_cast<const MTile*>(ws + L.thin);
+    return f;
 }
 
 // Fat tiles need a route list of at least fat_threshold rows, and a token
@@ -1399,8 +1434,9 @@ hipError_t launch_ffn_phase(const FfnLaunch& a, int phase, hipStream_t s) {
     DevInfo d;
     hipError_t err = dev_info(d);
     if (err != hipSuccess) return err;
-    const FfnArgs fa = make_args(a);
     const bool fat = a.T >= a.fat_threshold;
+    if (a.wfmt == 4) return launch_fp8_phase(make_fp8_args(a), phase, d.cus, fat, s);
+    const FfnArgs fa = make_args(a);
     // formats 0 and 2 (bf16, plain or row-pair layout) share the kernels
     if (phase == 1) return a.wfmt != 1 ? launch_phase_t<1, 0>(fa, d, fat, s) : launch_phase_t<1, 1>(fa, d, fat, s);
     return a.wfmt != 1 ? launch_phase_t<2, 0>(fa, d, fat, s) : launch_phase_t<2, 1>(fa, d, fat, s);

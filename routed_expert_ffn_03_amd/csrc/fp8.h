@@ -1,0 +1,96 @@
+// e4m3 helpers and kernel arguments of the 8-bit expert format (internal
+// header).
+//
+// Operands are e4m3 codes (1 sign, 4 exponent, 3 mantissa bits, largest
+// finite value 448, no infinities) with one fp32 scale per 128 columns of an
+// activation row and per 128 x 128 block of a weight matrix; a value is
+// code * scale.  A product over 128 columns is exact in the codes' fp32 MFMA
+// sum up to that sum's own rounding and takes both scales at once:
+//   y[i, n] = sum_b sx[i, b] sw[n / 128, b] sum_{k in b} xq[i, k] wq[n, k].
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "ffn_shared.h"
+
+namespace moe {
+
+constexpr int FP8_BLOCK = 128;
+constexpr float FP8_MAX = 448.0f;
+
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+
+// 32 x 32 x 64 e4m3 products without hardware scales: lane L holds row (A)
+// or column (B) L % 32 and 32 bytes of k; any assignment of k to the lanes'
+// bytes will do that A and B share.  Result element i of lane L is row
+// 8 (i / 4) + 4 (L / 32) + i % 4, column L % 32.
+__device__ __forceinline__ f32x16 mfma_fp8(i32x8 a, i32x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 pack8(u32x4 lo, u32x4 hi) {
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// |v| where it is finite, else 0: what a block's scale is taken from.
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a < __uint_as_float(0x7f800000u) ? a : 0.0f;         // (false for NaN too)
+}
+
+// The scale of a block whose largest finite magnitude is `top`: the least
+// power of two s >= 2^-126 with top <= 448 s, and 1 for top = 0.  A power of
+// two makes v / s exact, so the code of every value is the same in any
+// precision; e4m3 keeps its relative step over 14 octaves, so against
+// top / 448 this costs at most one octave at the small end.
+// top = 2^(p - 127) (1 + f): 448 = 2^8 * 1.75, so the exponent is p - 8, plus
+// one where 1 + f > 1.75.  Subnormal tops end at the lower limit.
+__device__ __forceinline__ float fp8_scale(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return top > 0.0f ? __uint_as_float((uint32_t)max(e, 1) << 23) : 1.0f;
+}
+
+// 1 / s for a power of two s in [2^-126, 2^126].
+__device__ __forceinline__ float pow2_rcp(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
+
+// Four values (already divided by the scale) as e4m3 codes, nearest even;
+// non-finite values become the NaN code.
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+    return (uint32_t)v;
+}
+
+struct Fp8Args {
+    const uint16_t* x;                  // bf16 [T, H]
+    const uint8_t* wg;                  // e4m3 [E, I, H]
+    const uint8_t* wu;
+    const uint8_t* wd;                  // e4m3 [E, H, I]
+    const float* sg;                    // fp32 [E, I/128, H/128]
+    const float* su;
+    const float* sd;                    // fp32 [E, H/128, I/128]
+    const int32_t* sorted_pair;
+    int T, k, H, I, E;
+    uint8_t* xq;                        // e4m3 [T, H] and its scales [T, H/128]
+    float* xs;
+    uint8_t* act;                       // e4m3 [T*k, I] and its scales [T*k, I/128]
+    float* as;
+    uint16_t* y;                        // fp16 [T*k, H]
+    const FfnHeader* hdr;
+    const MTile* fat;
+    const MTile* thin;
+};
+
+// e4m3 codes and scales of bf16 matrices (fp8_quant.hip): block_rows 1 (rows
+// of activations) or 128 (weights).
+hipError_t launch_quantize_fp8(const uint16_t* src, int64_t mats, int rows, int cols, int block_rows, uint8_t* codes,
+                               float* scales, hipStream_t s);
+
+// One phase of the grouped FFN on e4m3 weights (fp8_ffn.hip): 1 = gate/up
+// (quantises x first), 2 = down.  `fat` false: no route list can be fat.
+hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipStream_t s);
+
+}  // namespace moe
