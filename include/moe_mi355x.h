@@ -92,7 +92,9 @@ const char* moe_version(void);
  * thin experts' activation rows and their 128-group sums.  MOE_WFMT_FP8_B128
  * keeps the activation a in T*k*I + T*k*(I/128)*4 bytes (e4m3 codes, fp32
  * scales; the others: T*k*I*2) and needs T*H + T*(H/128)*4 more for the codes
- * and scales of x (each part rounded up to 256).  Returns 0 for
+ * and scales of x and T*k*(H/128)*4 for those scales in sorted order (each
+ * part rounded up to 256); it cuts fat lists into M-tiles of 224 rows, not
+ * 256.  Returns 0 for
  * arguments that are invalid or unsupported.  Alignment: 256 bytes (any
  * hipMalloc pointer).
  */

@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "fat8.hip", "stream.hip", "front.hip", "q3dec.hip", "combine.hip", "pack.hip",
-           "fp8_quant.hip", "fp8_ffn.hip", "balance.hip", "combine_bwd.hip"]
+           "fp8_quant.hip", "fp8_ffn.hip", "fp8_fat.hip", "balance.hip", "combine_bwd.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

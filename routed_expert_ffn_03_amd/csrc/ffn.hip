@@ -60,7 +60,7 @@ namespace {
 // ------------------------------------------------------------ tile builder
 
 __global__ __launch_bounds__(1024)
-void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, FfnHeader* __restrict__ hdr,
+void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, int bm, FfnHeader* __restrict__ hdr,
                         MTile* __restrict__ fat, MTile* __restrict__ thin, int32_t* __restrict__ counts) {
     __shared__ int scratch[16];
     const int e = threadIdx.x;
@@ -69,7 +69,7 @@ void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, Ffn
         r0 = offsets[e];
         n = offsets[e + 1] - r0;
         if (counts) counts[e] = n;                       // the load histogram, when asked for
-        if (n >= thr) nf = (n + FAT_BM - 1) / FAT_BM;
+        if (n >= thr) nf = (n + bm - 1) / bm;                // M-tiles of up to bm rows
         else nt = (n + THIN_BM - 1) / THIN_BM;
     }
     const int fi = block_inclusive_scan(nf, scratch);
@@ -1212,8 +1212,11 @@ void ffn_thin_q3_kernel(FfnArgs a) {
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// rows per fat M-tile
+int fat_bm(int wfmt) { return wfmt == 4 ? FP8_BM : FAT_BM; }
+
 struct FfnLayout {
-    size_t hdr, fat, thin, act, as, xq, xs, total;
+    size_t hdr, fat, thin, act, as, xq, xs, xst, total;
     size_t max_fat, max_thin;
 };
 
@@ -1221,7 +1224,7 @@ FfnLayout ffn_layout(int T, int E, int k, int H, int I, int wfmt) {
     const size_t P = (size_t)T * k;
     const size_t nz = P < (size_t)E ? P : (size_t)E;        // experts that can be non-empty
     FfnLayout L;
-    L.max_fat = P / FAT_BM + nz + 1;
+    L.max_fat = P / fat_bm(wfmt) + nz + 1;
     L.max_thin = P / THIN_BM + nz + 1;
     L.hdr = 0;
     L.fat = align256(sizeof(FfnHeader));
@@ -1232,10 +1235,12 @@ FfnLayout ffn_layout(int T, int E, int k, int H, int I, int wfmt) {
         L.as = L.act + align256(P * (size_t)I);
         L.xq = L.as + align256(P * (size_t)(I / 128) * sizeof(float));
         L.xs = L.xq + align256((size_t)T * H);
-        L.total = L.xs + align256((size_t)T * (H / 128) * sizeof(float));
+        L.xst = L.xs + align256((size_t)T * (H / 128) * sizeof(float));
+        L.total = L.xst + align256(P * (size_t)(H / 128) * sizeof(float));
         return L;
     }
     L.xq = L.as = L.act + align256(P * (size_t)I * sizeof(uint16_t));
+    L.xst = 0;
     // 3-bit weights: reordered x rows and group sums for the thin gate/up path
     const size_t xq_bytes = wfmt == 1 ? align256((size_t)T * H * sizeof(uint16_t)) : 0;
     L.xs = L.xq + xq_bytes;
@@ -1350,6 +1355,7 @@ Fp8Args make_fp8_args(const FfnLaunch& a) {
     f.T = a.T; f.k = a.k; f.H = a.H; f.I = a.I; f.E = a.E;
     f.xq = reinterpret_cast<uint8_t*>(ws + L.xq);
     f.xs = reinterpret_cast<float*>(ws + L.xs);
+    f.xst = reinterpret_cast<float*>(ws + L.xst);
     f.act = reinterpret_cast<uint8_t*>(ws + L.act);
     f.as = reinterpret_cast<float*>(ws + L.as);
     f.y = a.y;
@@ -1423,7 +1429,7 @@ FfnPlanPtrs ffn_plan_ptrs(int T, int E, int k, int H, int I, int wfmt, void* ffn
 hipError_t launch_ffn_plan(const FfnLaunch& a, hipStream_t s) {
     const FfnLayout L = ffn_layout(a.T, a.E, a.k, a.H, a.I, a.wfmt);
     char* ws = reinterpret_cast<char*>(a.ws);
-    build_tiles_kernel<<<1, 1024, 0, s>>>(a.offsets, a.E, a.fat_threshold,
+    build_tiles_kernel<<<1, 1024, 0, s>>>(a.offsets, a.E, a.fat_threshold, fat_bm(a.wfmt),
                                           reinterpret_cast<FfnHeader*>(ws + L.hdr),
                                           reinterpret_cast<MTile*>(ws + L.fat),
                                           reinterpret_cast<MTile*>(ws + L.thin), a.counts);

@@ -18,7 +18,7 @@
 namespace moe {
 
 constexpr int FP8_BLOCK = 128;
-constexpr float FP8_MAX = 448.0f;
+constexpr int FP8_BM = 224;              // rows per MFMA M-tile: leaves LDS for the row scales (fp8_fat.hip)
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
@@ -76,7 +76,8 @@ struct Fp8Args {
     int T, k, H, I, E;
     uint8_t* xq;                        // e4m3 [T, H] and its scales [T, H/128]
     float* xs;
-    uint8_t* act;                       // e4m3 [T*k, I] and its scales [T*k, I/128]
+    float* xst;                         // the scales of x by sorted row, [H/128, T*k] (MFMA tiles only)
+    uint8_t* act;                       // e4m3 [T*k, I] and its scales [I/128, T*k]
     float* as;
     uint16_t* y;                        // fp16 [T*k, H]
     const FfnHeader* hdr;
@@ -92,5 +93,8 @@ hipError_t launch_quantize_fp8(const uint16_t* src, int64_t mats, int rows, int 
 // One phase of the grouped FFN on e4m3 weights (fp8_ffn.hip): 1 = gate/up
 // (quantises x first), 2 = down.  `fat` false: no route list can be fat.
 hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipStream_t s);
+
+// ... over the MFMA M-tiles only (fp8_fat.hip)
+hipError_t launch_fp8_fat_phase(const Fp8Args& a, int phase, int cus, hipStream_t s);
 
 }  // namespace moe

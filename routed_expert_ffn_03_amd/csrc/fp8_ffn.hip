@@ -36,10 +36,11 @@ void ffn_fp8_rows_kernel(Fp8Args a) {
     const int K = PHASE == 1 ? a.H : a.I, N = PHASE == 1 ? a.I : a.H;
     const int KB = K / FP8_BLOCK;
     const int NT = PHASE == 1 ? N / 128 : N / 256;
-    const int n_fat = a.hdr->n_fat, n_tiles = n_fat + a.hdr->n_thin;
+    const int n_tiles = a.hdr->n_thin;
+    const size_t P = (size_t)a.T * a.k;
     for (int item = blockIdx.x; item < n_tiles * NT; item += gridDim.x) {
         const int q = item / NT, nt = item - q * NT;
-        const MTile t = q < n_fat ? a.fat[q] : a.thin[q - n_fat];
+        const MTile t = a.thin[q];
         const size_t eoff = (size_t)t.e * N * K;
         const size_t soff = (size_t)t.e * (N / FP8_BLOCK) * KB;
         // this lane's weight row and the scale rows of its block(s)
@@ -48,12 +49,13 @@ void ffn_fp8_rows_kernel(Fp8Args a) {
         const float* s0 = PHASE == 1 ? a.sg + soff + (size_t)nt * KB
                                      : a.sd + soff + (size_t)((nt * 256 + 32 * wave) / FP8_BLOCK) * KB;
         const float* s1 = PHASE == 1 ? a.su + soff + (size_t)nt * KB : s0;
-        for (int r0 = 0; r0 < t.rows; r0 += 32) {
+        {
             // rows past the tile repeat its last one; they are never stored
-            const int row = t.row0 + min(r0 + m, t.rows - 1);
+            const int row = t.row0 + min(m, t.rows - 1);
             const size_t src = PHASE == 1 ? (size_t)(a.sorted_pair[row] / a.k) : (size_t)row;
             const uint8_t* x = (PHASE == 1 ? a.xq : a.act) + src * K + 32 * g;
-            const float* xs = (PHASE == 1 ? a.xs : a.as) + src * KB;
+            const float* xs = PHASE == 1 ? a.xs + src * KB : a.as + src;
+            const size_t xstep = PHASE == 1 ? 1 : P;
             f32x16 acc = f32x16{};
             for (int b = 0; b < KB; ++b) {
                 f32x16 part = f32x16{};
@@ -63,7 +65,7 @@ void ffn_fp8_rows_kernel(Fp8Args a) {
                     const uint8_t* xp = x + b * FP8_BLOCK + 64 * h;
                     part = mfma_fp8(pack8(ldg16(wp), ldg16(wp + 16)), pack8(ldg16(xp), ldg16(xp + 16)), part);
                 }
-                const float sx = xs[b];
+                const float sx = xs[b * xstep];
                 const float f0 = sx * s0[b], f1 = PHASE == 1 ? sx * s1[b] : f0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i] = fmaf(part[i], i < 8 ? f0 : f1, acc[i]);
@@ -82,15 +84,15 @@ void ffn_fp8_rows_kernel(Fp8Args a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) tp = fmaxf(tp, top[i][m]);
                 const float s = fp8_scale(tp), r = pow2_rcp(s);
-                if (r0 + m < t.rows) {
+                if (m < t.rows) {
                     uint8_t* dst = a.act + (size_t)row * a.I + nt * 128 + 16 * wave + 4 * g;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         *reinterpret_cast<uint32_t*>(dst + 8 * i) =
                             fp8_pack4(v[4 * i] * r, v[4 * i + 1] * r, v[4 * i + 2] * r, v[4 * i + 3] * r);
-                    if (wave == 0 && g == 0) a.as[(size_t)row * (a.I / FP8_BLOCK) + nt] = s;
+                    if (wave == 0 && g == 0) a.as[(size_t)nt * P + row] = s;
                 }
-            } else if (r0 + m < t.rows) {
+            } else if (m < t.rows) {
                 uint16_t* dst = a.y + (size_t)row * a.H + nt * 256 + 32 * wave + 4 * g;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -107,10 +109,15 @@ void ffn_fp8_rows_kernel(Fp8Args a) {
 }  // namespace
 
 hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipStream_t s) {
-    (void)fat;
     if (phase == 1) {
         const hipError_t err = launch_quantize_fp8(a.x, 1, a.T, a.H, 1, a.xq, a.xs, s);
         if (err != hipSuccess) return err;
+    }
+    if (fat) {
+        const hipError_t err = launch_fp8_fat_phase(a, phase, cus, s);
+        if (err != hipSuccess) return err;
+    }
+    if (phase == 1) {
         ffn_fp8_rows_kernel<1><<<2 * cus, F8S_THREADS, 0, s>>>(a);
     } else {
         ffn_fp8_rows_kernel<2><<<2 * cus, F8S_THREADS, 0, s>>>(a);

@@ -124,8 +124,8 @@ def L():
 def test_fp8_workspace_size(L):
     r = lambda v: (v + 255) // 256 * 256
     T, E, k, H, I = 100, 16, 2, 512, 384
-    lists = L.moe_workspace_size(T, E, k, H, I, 0) - r(T * k * I * 2)
-    want = lists + r(T * k * I) + r(T * k * (I // 128) * 4) + r(T * H) + r(T * (H // 128) * 4)
+    lists = L.moe_workspace_size(T, E, k, H, I, 0) - r(T * k * I * 2)       # (T k < 224: the same lists)
+    want = lists + r(T * k * I) + r(T * k * (I // 128) * 4) + r(T * H) + r(T * (H // 128) * 4) + r(T * k * (H // 128) * 4)
     assert L.moe_workspace_size(T, E, k, H, I, 4) == want
     assert L.moe_workspace_size(T, E, k, H, I + 64, 4) == 0
     assert L.moe_workspace_size(T, E, k, H, I, 3) == 0
