@@ -4,106 +4,196 @@
 //   aq, sa = e4m3 rows of a
 //   y      = aq Wd^T, stored fp16
 // with every 128-column partial product taken in fp32 on the MFMA and
-// multiplied by its two scales before it is added (fp8.h).
+// multiplied by its two scales before it is added (fp8.h).  Busy experts run
+// as MFMA tiles (fp8_fat.hip); here are the phases and the streaming kernel of
+// the short route lists, which includes all of a decode step.
 //
 // The weights are the MFMA's A operand and the activation rows its B operand,
 // so that a lane's result registers all belong to one activation row: the row
-// scale is one value per lane, the weight scale one value per wave, and four
-// consecutive result registers are four consecutive output columns.
+// scale is one value per lane, the weight scale one value per column tile, and
+// four consecutive result registers are four consecutive output columns.
 //
-// Work item: (32 rows of a route list, 128 columns of a or 256 of y), one
-// 512-thread block; wave w owns 16 gate and the matching 16 up rows (phase 1)
-// or 32 rows of W_down (phase 2) over the whole reduction index, so no
-// partial sums cross waves; phase 1 exchanges the row maxima of its 128
-// columns, which are one scale group of a, and stores codes.
+// Streaming kernel.  Work item: (a tile of up to 32 rows, 128 columns of a or
+// 256 of y), one 256-thread block; wave w owns 32 gate and the matching 32 up
+// rows (phase 1) or 64 rows of W_down (phase 2) over the whole reduction
+// index, so no partial sums cross waves; phase 1 exchanges the row maxima of
+// its 128 columns, which are one scale group of a, and stores codes.  Every
+// weight is used once, so it is bound by HBM reads: a wave streams its 64 rows
+// through its own two-slot LDS ring, one 128-column block (8 KB) in flight
+// while the one before is multiplied, by direct-to-LDS loads of 8 rows x 128
+// bytes with the non-temporal hint (whole lines).  The first block of the next
+// item is in flight over the epilogue.  Activation rows come straight into
+// registers; they are a few KB that stay in L2.
 #include "common.h"
 #include "ffn_shared.h"
 #include "fp8.h"
 #include "kernels.h"
+#include "lds_dma.h"
 
 namespace moe {
 namespace {
 
-constexpr int F8S_THREADS = 512;
+constexpr int FS_THREADS = 256;
+constexpr uint32_t FS_CHUNK = 64 * 128;              // a wave's 64 weight rows of one block
+constexpr int FS_SLOTS = 2;
+constexpr uint32_t FS_RING = 4 * FS_SLOTS * FS_CHUNK;
 
 template <int PHASE>
-__global__ __launch_bounds__(F8S_THREADS)
-void ffn_fp8_rows_kernel(Fp8Args a) {
-    __shared__ float top[8][32];
+__global__ __launch_bounds__(FS_THREADS, 2)
+void ffn_fp8_stream_kernel(Fp8Args a) {
+    __shared__ __attribute__((aligned(1024))) char ring[FS_RING];
+    __shared__ float top[2][4][32];                  // phase 1: row maxima by wave, alternating between items
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m = lane & 31, g = lane >> 5;
     const int K = PHASE == 1 ? a.H : a.I, N = PHASE == 1 ? a.I : a.H;
     const int KB = K / FP8_BLOCK;
     const int NT = PHASE == 1 ? N / 128 : N / 256;
-    const int n_tiles = a.hdr->n_thin;
+    const int n_mt = a.hdr->n_thin;
+    const int n_items = n_mt * NT;
     const size_t P = (size_t)a.T * a.k;
-    for (int item = blockIdx.x; item < n_tiles * NT; item += gridDim.x) {
-        const int q = item / NT, nt = item - q * NT;
-        const MTile t = a.thin[q];
-        const size_t eoff = (size_t)t.e * N * K;
-        const size_t soff = (size_t)t.e * (N / FP8_BLOCK) * KB;
-        // this lane's weight row and the scale rows of its block(s)
-        const int wrow = PHASE == 1 ? nt * 128 + 16 * wave + (m & 15) : nt * 256 + 32 * wave + m;
-        const uint8_t* w = (PHASE == 1 ? (m < 16 ? a.wg : a.wu) : a.wd) + eoff + (size_t)wrow * K + 32 * g;
-        const float* s0 = PHASE == 1 ? a.sg + soff + (size_t)nt * KB
-                                     : a.sd + soff + (size_t)((nt * 256 + 32 * wave) / FP8_BLOCK) * KB;
-        const float* s1 = PHASE == 1 ? a.su + soff + (size_t)nt * KB : s0;
-        {
-            // rows past the tile repeat its last one; they are never stored
-            const int row = t.row0 + min(m, t.rows - 1);
-            const size_t src = PHASE == 1 ? (size_t)(a.sorted_pair[row] / a.k) : (size_t)row;
-            const uint8_t* x = (PHASE == 1 ? a.xq : a.act) + src * K + 32 * g;
-            const float* xs = PHASE == 1 ? a.xs + src * KB : a.as + src;
-            const size_t xstep = PHASE == 1 ? 1 : P;
-            f32x16 acc = f32x16{};
-            for (int b = 0; b < KB; ++b) {
-                f32x16 part = f32x16{};
+    const size_t wbytes = (size_t)N * K;
+    int item = blockIdx.x;
+    if (item >= n_items) return;                     // the whole block
+
+    // (read-only here: through the constant address space, so by scalar loads,
+    // which leave the vector loads' count alone)
+    typedef const __attribute__((address_space(4))) MTile* ctile_t;
+    typedef const __attribute__((address_space(4))) float* cfloat_t;
+    struct Item {
+        int e, row0, rows, nt;
+    };
+    auto load_item = [&](int it) {                   // items past the end are clamped: valid addresses, never used
+        const int ic = min(it, n_items - 1), nt = ic / n_mt;
+        const ctile_t tp = (ctile_t)a.thin + __builtin_amdgcn_readfirstlane(ic - nt * n_mt);
+        return Item{tp->e, tp->row0, tp->rows, nt};
+    };
+    // load instruction i moves rows 8 i .. 8 i + 7: lane L row L / 8, position
+    // L % 8, which holds piece (L % 8) ^ (row & 7) ^ ((row >> 3) & 1)
+    const int lr = lane >> 3;
+    uint32_t po[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* wp = w + b * FP8_BLOCK + 64 * h;
-                    const uint8_t* xp = x + b * FP8_BLOCK + 64 * h;
-                    part = mfma_fp8(pack8(ldg16(wp), ldg16(wp + 16)), pack8(ldg16(xp), ldg16(xp + 16)), part);
-                }
-                const float sx = xs[b * xstep];
-                const float f0 = sx * s0[b], f1 = PHASE == 1 ? sx * s1[b] : f0;
+    for (int i = 0; i < 2; ++i) po[i] = (uint32_t)(((lane & 7) ^ lr ^ i) * 16);
+    auto issue_w = [&](const Item& q, int ch, int sl) {
+        const size_t eoff = (size_t)q.e * wbytes;
+        const __amdgpu_buffer_rsrc_t w0 = make_rsrc((PHASE == 1 ? a.wg : a.wd) + eoff, (uint32_t)wbytes);
+        const __amdgpu_buffer_rsrc_t w1 = PHASE == 1 ? make_rsrc(a.wu + eoff, (uint32_t)wbytes) : w0;
+        const uint32_t r0 = (uint32_t)(PHASE == 1 ? q.nt * 128 + 32 * wave : q.nt * 256 + 64 * wave) + lr;
+        char* st = ring + (wave * FS_SLOTS + sl) * FS_CHUNK;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = fmaf(part[i], i < 8 ? f0 : f1, acc[i]);
+        for (int i = 0; i < 8; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < 4 ? w0 : w1, (lds_ptr_t)(st + i * 1024), 16,
+                                                     (r0 + 8 * (PHASE == 1 ? i & 3 : i)) * (uint32_t)K + po[i & 1],
+                                                     ch * FP8_BLOCK, 0, 2);
+    };
+    // fragment reads: lane (m, g), half h of the block, 16 bytes j: piece 4 h + 2 g + j of row m
+    const uint32_t base = lds_addr(ring) + (uint32_t)(wave * FS_SLOTS) * FS_CHUNK + (uint32_t)m * 128;
+    uint32_t fo[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fo[h][j] = base + (uint32_t)(((4 * h + 2 * g + j) ^ (m & 7) ^ ((m >> 3) & 1)) * 16);
+
+    Item cur = load_item(item);
+    issue_w(cur, 0, 0);
+    for (int sl = 0, par = 0;; par ^= 1) {
+        const Item nxt = load_item(item + gridDim.x);
+        // rows past the tile repeat its last one; they are never stored
+        const int row = cur.row0 + min(m, cur.rows - 1);
+        const size_t src = PHASE == 1 ? (size_t)(a.sorted_pair[row] / a.k) : (size_t)row;
+        const uint8_t* x = (PHASE == 1 ? a.xq : a.act) + src * K + 32 * g;
+        const float* xs = PHASE == 1 ? a.xs + src * KB : a.as + src;
+        const size_t xstep = PHASE == 1 ? 1 : P;
+        const size_t soff = (size_t)cur.e * (N / FP8_BLOCK) * KB;
+        const cfloat_t s0 = (cfloat_t)(PHASE == 1 ? a.sg + soff + (size_t)cur.nt * KB
+                                                  : a.sd + soff + (size_t)(2 * cur.nt + (wave >> 1)) * KB);
+        const cfloat_t s1 = PHASE == 1 ? (cfloat_t)(a.su + soff + (size_t)cur.nt * KB) : s0;
+        u32x4 xf[2][2];
+        float sx;
+        auto issue_x = [&](int ch) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) xf[h][j] = ldg16(x + ch * FP8_BLOCK + 64 * h + 16 * j);
+            sx = xs[ch * xstep];
+        };
+        f32x16 acc[2] = {f32x16{}, f32x16{}};
+        issue_x(0);
+        for (int ch = 0; ch < KB; ++ch) {
+            // the block after this one (of the next item at the end; past the
+            // last item a repeat that nobody reads), then everything older
+            const bool end = ch + 1 == KB;
+            issue_w(end ? nxt : cur, end ? 0 : ch + 1, sl ^ 1);
+            const float f0 = s0[ch], f1 = s1[ch];
+            vm_wait<8>();
+            const uint32_t so = (uint32_t)sl * FS_CHUNK;
+            u32x4 w[2][2][2];
+            static_for<2>([&](auto h_c) {
+                static_for<2>([&](auto j_c) {
+                    constexpr int Hh = decltype(h_c)::value, J = decltype(j_c)::value;
+                    w[0][Hh][J] = ds_read16<0>(fo[Hh][J] + so);
+                    w[1][Hh][J] = ds_read16<32 * 128>(fo[Hh][J] + so);
+                });
+            });
+            lds_wait_all();
+            static_for<2>([&](auto h_c) {
+                static_for<2>([&](auto j_c) {
+                    constexpr int Hh = decltype(h_c)::value, J = decltype(j_c)::value;
+                    tie_after_wait(w[0][Hh][J]);
+                    tie_after_wait(w[1][Hh][J]);
+                });
+            });
+            const i32x8 x0 = pack8(xf[0][0], xf[0][1]), x1 = pack8(xf[1][0], xf[1][1]);
+            f32x16 p0 = mfma_fp8(pack8(w[0][0][0], w[0][0][1]), x0, f32x16{});
+            f32x16 p1 = mfma_fp8(pack8(w[1][0][0], w[1][0][1]), x0, f32x16{});
+            p0 = mfma_fp8(pack8(w[0][1][0], w[0][1][1]), x1, p0);
+            p1 = mfma_fp8(pack8(w[1][1][0], w[1][1][1]), x1, p1);
+            const float g0 = sx * f0, g1 = PHASE == 1 ? sx * f1 : g0;
+            issue_x(min(ch + 1, KB - 1));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                acc[0][r] = fmaf(p0[r], g0, acc[0][r]);
+                acc[1][r] = fmaf(p1[r], g1, acc[1][r]);
             }
-            if constexpr (PHASE == 1) {
-                float v[8], tp = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = silu_mul(acc[i], acc[i + 8]);
-                    tp = fmaxf(tp, finite_abs(v[i]));
-                }
-                tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
-                __syncthreads();
-                if (g == 0) top[wave][m] = tp;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) tp = fmaxf(tp, top[i][m]);
-                const float s = fp8_scale(tp), r = pow2_rcp(s);
-                if (m < t.rows) {
-                    uint8_t* dst = a.act + (size_t)row * a.I + nt * 128 + 16 * wave + 4 * g;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint32_t*>(dst + 8 * i) =
-                            fp8_pack4(v[4 * i] * r, v[4 * i + 1] * r, v[4 * i + 2] * r, v[4 * i + 3] * r);
-                    if (wave == 0 && g == 0) a.as[(size_t)nt * P + row] = s;
-                }
-            } else if (m < t.rows) {
-                uint16_t* dst = a.y + (size_t)row * a.H + nt * 256 + 32 * wave + 4 * g;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint2 o;
-                    o.x = (uint32_t)f32_to_f16_bits(acc[4 * i]) | ((uint32_t)f32_to_f16_bits(acc[4 * i + 1]) << 16);
-                    o.y = (uint32_t)f32_to_f16_bits(acc[4 * i + 2]) | ((uint32_t)f32_to_f16_bits(acc[4 * i + 3]) << 16);
-                    *reinterpret_cast<uint2*>(dst + 8 * i) = o;
-                }
-            }
+            sl ^= 1;
         }
+        if constexpr (PHASE == 1) {
+            float tp = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                acc[0][r] = silu_mul(acc[0][r], acc[1][r]);
+                tp = fmaxf(tp, finite_abs(acc[0][r]));
+            }
+            tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
+            if (g == 0) top[par][wave][m] = tp;
+            lds_barrier();                           // (the next item's weights stay in flight)
+            const float s = fp8_scale(fmaxf(fmaxf(top[par][0][m], top[par][1][m]), fmaxf(top[par][2][m], top[par][3][m])));
+            const float r = pow2_rcp(s);
+            if (m < cur.rows) {
+                uint8_t* dst = a.act + (size_t)row * a.I + cur.nt * 128 + 32 * wave + 4 * g;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint32_t*>(dst + 8 * j) =
+                        fp8_pack4(acc[0][4 * j] * r, acc[0][4 * j + 1] * r, acc[0][4 * j + 2] * r, acc[0][4 * j + 3] * r);
+                if (wave == 0 && g == 0) a.as[(size_t)cur.nt * P + row] = s;
+            }
+        } else if (m < cur.rows) {
+            uint16_t* dst = a.y + (size_t)row * a.H + cur.nt * 256 + 64 * wave + 4 * g;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint2 o;
+                    o.x = (uint32_t)f32_to_f16_bits(acc[c][4 * j]) | ((uint32_t)f32_to_f16_bits(acc[c][4 * j + 1]) << 16);
+                    o.y = (uint32_t)f32_to_f16_bits(acc[c][4 * j + 2]) | ((uint32_t)f32_to_f16_bits(acc[c][4 * j + 3]) << 16);
+                    *reinterpret_cast<uint2*>(dst + 32 * c + 8 * j) = o;
+                }
+        }
+        item += gridDim.x;
+        if (item >= n_items) break;
+        cur = nxt;
     }
+    vm_wait<0>();                                    // the unused last block has landed
 }
 
 }  // namespace
@@ -117,11 +207,8 @@ hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipS
         const hipError_t err = launch_fp8_fat_phase(a, phase, cus, s);
         if (err != hipSuccess) return err;
     }
-    if (phase == 1) {
-        ffn_fp8_rows_kernel<1><<<2 * cus, F8S_THREADS, 0, s>>>(a);
-    } else {
-        ffn_fp8_rows_kernel<2><<<2 * cus, F8S_THREADS, 0, s>>>(a);
-    }
+    if (phase == 1) ffn_fp8_stream_kernel<1><<<2 * cus, FS_THREADS, 0, s>>>(a);
+    else ffn_fp8_stream_kernel<2><<<2 * cus, FS_THREADS, 0, s>>>(a);
     return hipGetLastError();
 }
 
