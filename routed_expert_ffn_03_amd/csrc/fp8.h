@@ -18,7 +18,7 @@
 namespace moe {
 
 constexpr int FP8_BLOCK = 128;
-constexpr int FP8_BM = 224;              // rows per MFMA M-tile: leaves LDS for the row scales (fp8_fat.hip)
+constexpr int FP8_BM = 192;              // rows per MFMA M-tile: leaves LDS for the row scales (fp8_fat.hip)
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
@@ -28,6 +28,13 @@ typedef __attribute__((ext_vector_type(8))) int i32x8;
 // 8 (i / 4) + 4 (L / 32) + i % 4, column L % 32.
 __device__ __forceinline__ f32x16 mfma_fp8(i32x8 a, i32x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// 16 x 16 x 128 e4m3 products: lane L holds row (A) or column (B) L % 16 and
+// 32 bytes of k.  Result element i of lane L is row 4 (L / 16) + i, column
+// L % 16.
+__device__ __forceinline__ f32x4 mfma16_fp8(i32x8 a, i32x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ i32x8 pack8(u32x4 lo, u32x4 hi) {

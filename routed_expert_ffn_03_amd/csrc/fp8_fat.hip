@@ -43,13 +43,25 @@ constexpr uint32_t FF_A = FP8_BM * FF_ROW;                 // activation slot
 constexpr int FF_NW = 3, FF_NA = 2;
 constexpr uint32_t FF_A0 = FF_NW * FF_W;                   // LDS offsets
 constexpr uint32_t FF_S0 = FF_A0 + FF_NA * FF_A;
-constexpr uint32_t FF_LDS = FF_S0 + FF_NA * 256 * 4;
+constexpr uint32_t FF_S = 256 * 4 + 256;                   // scale slot: 256 row scales, then the two block scales
+constexpr uint32_t FF_T0 = FF_S0 + FF_NA * FF_S;           // row maxima of the four column groups
+constexpr uint32_t FF_LDS = FF_T0 + 4 * 256 * 4;
 static_assert(FF_LDS <= 160 * 1024, "LDS of one CU");
+static_assert(FP8_BM <= 192, "at most six 16-row tiles for a wave");
 
-// Row pitch of the epilogue staging tile in bytes (16 of padding).
-template <int PHASE>
-constexpr uint32_t ff_pitch() { return (PHASE == 1 ? 128 : 512) + 16; }
-static_assert(FP8_BM * ff_pitch<2>() <= FF_LDS && FP8_BM * ff_pitch<1>() + 4 * 256 * 4 <= FF_LDS, "staging");
+// Exchanges between lanes that differ in lane bit 5 (or 4): afterwards a lane
+// with that bit clear holds both lanes' a, one with it set both lanes' b (in
+// the order of the bit).
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
 
 template <int PHASE>
 __global__ __launch_bounds__(FF_THREADS, 1)
@@ -59,7 +71,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = wave >> 2, q = wave & 3;
-    const int m = lane & 31, g = lane >> 5;
+    const int m = lane & 15, kg = lane >> 4;
     const int K = PHASE == 1 ? a.H : a.I, N = PHASE == 1 ? a.I : a.H;
     const int KB = K / FP8_BLOCK;
     constexpr int BN = PHASE == 1 ? 128 : 256;
@@ -69,35 +81,28 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     const size_t wbytes = (size_t)N * K;
     const __amdgpu_buffer_rsrc_t asrc = PHASE == 1 ? make_rsrc(a.xq, (uint32_t)((size_t)a.T * K))
                                                    : make_rsrc(a.act, (uint32_t)(P * K));
-    const __amdgpu_buffer_rsrc_t ssrc = make_rsrc(PHASE == 1 ? a.xst : a.as, (uint32_t)(P * KB * 4));
+    typedef const __attribute__((address_space(1))) void* gptr_t;
     const uint32_t sbase = lds_addr(smem);
     // a load instruction moves rows 8 j .. 8 j + 7: lane L row L / 8, position L % 8
     const int lr = lane >> 3;
     auto piece = [&](int row) { return (uint32_t)(((lane & 7) ^ (row & 7) ^ ((row >> 3) & 1)) * 16); };
-    // fragment reads: lane (m, g), half h of the stage, 16 bytes j: piece 4 h + 2 g + j of row m
-    uint32_t fo[2][2];
+    // fragment reads: lane (m, kg), 16 bytes j: piece 2 kg + j of row m
+    uint32_t fo[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            fo[h][j] = (uint32_t)m * FF_ROW + (uint32_t)(((4 * h + 2 * g + j) ^ (m & 7) ^ ((m >> 3) & 1)) * 16);
+    for (int j = 0; j < 2; ++j)
+        fo[j] = sbase + (uint32_t)m * FF_ROW + (uint32_t)(((2 * kg + j) ^ (m & 7) ^ ((m >> 3) & 1)) * 16);
+    // column tiles 0, 1 and 2, 3 of this wave: 16 rows of W each (phase 1: gate rows 32 q .. and up rows 32 q ..;
+    // phase 2: rows 64 q ..)
     const uint32_t wfo = (uint32_t)(PHASE == 1 ? 32 * q : 64 * q) * FF_ROW;
-    constexpr int WC = (PHASE == 1 ? 128 : 32) * (int)FF_ROW;      // from the wave's first column tile to its second
+    constexpr int WC2 = (PHASE == 1 ? 128 : 32) * (int)FF_ROW;
 
     for (int item = logical_block(); item < n_items; item += gridDim.x) {
         MTile t;
         int nt;
         fat_item(a.fat, item, NT, t, nt);
-        const int rt = (t.rows + 31) >> 5;
+        const int tt = (t.rows + 15) >> 4;                         // 16-row tiles
         const uint8_t* wmat = PHASE == 1 ? (wave < 4 ? a.wg : a.wu) : a.wd;
         const __amdgpu_buffer_rsrc_t wsrc = make_rsrc(wmat + (size_t)t.e * wbytes, (uint32_t)wbytes);
-        // block scales of this wave's column tiles
-        const size_t soff = (size_t)t.e * (N / FP8_BLOCK) * KB;
-        // (read through the constant address space: scalar loads, which leave the vector loads' count alone)
-        typedef const __attribute__((address_space(4))) float* cfloat_t;
-        const cfloat_t sw0 = (cfloat_t)(PHASE == 1 ? a.sg + soff + (size_t)nt * KB
-                                                   : a.sd + soff + (size_t)(2 * nt + (q >> 1)) * KB);
-        const cfloat_t sw1 = PHASE == 1 ? (cfloat_t)(a.su + soff + (size_t)nt * KB) : sw0;
         // activation instruction j of this wave: tile rows 8 (8 j + wave) + L / 8 (rows past the M-tile repeat
         // its last one); weight instruction j: rows 32 wave + 8 j + L / 8 of the slot
         uint32_t aoff[4], woff[4];
@@ -111,184 +116,304 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             const uint32_t wrow = PHASE == 1 ? (uint32_t)(nt * 128 + (w & 127)) : (uint32_t)(nt * 256 + w);
             woff[j] = wrow * (uint32_t)K + piece(w);
         }
-        // row scales [KB][P]: lane L of wave w takes row 64 (w % 4) + L
-        const uint32_t srow = (uint32_t)(t.row0 + min(64 * q + lane, t.rows - 1)) * 4u;
+        const int na = 2 * tt;                                     // activation instructions of the block per stage
+        // Scales of stage kt, 4 bytes per lane: waves 0-3 the row scales, 64
+        // each, from the block-major array (position 8 (16 G + m) + t holds
+        // row 32 t + 16 G + m, so that a lane finds its tiles' scales in a
+        // row); wave 4 the two block scales of W (phase 1: gate, up; phase 2:
+        // those of the lower and, 8 bytes on, of the upper 128 columns)
+        const float* sp;
+        size_t sstep;
+        {
+            const int pos = 64 * q + lane, r = 32 * (pos & 7) + (pos >> 3);
+            const float* rows = (PHASE == 1 ? a.xst : a.as) + t.row0 + min(r, t.rows - 1);
+            const size_t soff = (size_t)t.e * (N / FP8_BLOCK) * KB;
+            const float* blocks = PHASE == 1 ? (lane == 0 ? a.sg : a.su) + soff + (size_t)nt * KB
+                                             : a.sd + soff + (size_t)(2 * nt + (lane < 2 ? 0 : 1)) * KB;
+            sp = wave < 4 ? rows : blocks;
+            sstep = wave < 4 ? P : 1;
+        }
+        auto issue_w = [&](int kt, int j) {                        // weight instruction j of stage kt
+            dma16(wsrc, lds + (kt % FF_NW) * FF_W + wave * 4096 + j * 1024, woff[j], kt * FF_ROW);
+        };
+        auto issue_a = [&](int kt, int j) {                        // activation instruction j, if the M-tile has its rows
+            if (8 * j + wave < na) dma16(asrc, lds + FF_A0 + (kt & 1) * FF_A + wave * 1024 + j * 8192, aoff[j], kt * FF_ROW);
+        };
+        auto issue_s = [&](int kt) {
+            if (wave < 5)
+                __builtin_amdgcn_global_load_lds((gptr_t)(sp + kt * sstep),
+                                                 (lds_ptr_t)(lds + FF_S0 + (kt & 1) * FF_S + wave * 256), 4, 0, 0);
+        };
+        auto barrier = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
 
-        auto kloop = [&](auto rt_c) {
-            constexpr int RT = decltype(rt_c)::value;
-            constexpr int LA = (RT + 1) / 2;                       // activation loads per wave per stage
-            auto issue_w = [&](int kt, int slot) {
-                char* st = lds + slot * FF_W + wave * 4096;
+        auto run = [&](auto rg_c) {
+            constexpr int RG = decltype(rg_c)::value;              // row tiles of this wave: G, G + 2, ...
+            constexpr int RA = RG > 0 ? RG : 1;
+            // ring of row fragments: a divisor of RG, so that a tile has the
+            // same registers in every stage, and three at least where reads
+            // run two tiles ahead (RG > 2)
+            constexpr int NB = RG % 3 == 0 ? 3 : RA;
+            f32x4 acc[RA][4], p[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dma16(wsrc, st + j * 1024, woff[j], kt * FF_ROW);
+            for (int c = 0; c < 4; ++c) {
+                p[c] = f32x4{};
+#pragma unroll
+                for (int i = 0; i < RA; ++i) acc[i][c] = f32x4{};
+            }
+            float f0 = 0.0f, f1 = 0.0f;                            // scales of the partial sums in p
+            u32x4 w[4][2], x[NB][2], sx0;                    // weights by column tile, rows in a ring of three tiles
+            u32x2 sx1, swv;                                        // row scales of tiles 0-3 and 4, 5; block scales
+            auto read_w = [&](auto c_c, int kt) {
+                constexpr int C = decltype(c_c)::value;
+                const uint32_t wb = (uint32_t)(kt % FF_NW) * FF_W + wfo;
+                w[C][0] = ds_read16<(C & 1) * 16 * (int)FF_ROW + (C >> 1) * WC2>(wb + fo[0]);
+                w[C][1] = ds_read16<(C & 1) * 16 * (int)FF_ROW + (C >> 1) * WC2>(wb + fo[1]);
             };
-            auto issue_a = [&](int kt, int slot) {
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ssrc, (lds_ptr_t)(lds + FF_S0 + slot * 1024 + q * 256), 4, srow,
-                                                         (uint32_t)(kt * P * 4), 0, 0);
-                char* st = lds + FF_A0 + slot * FF_A + wave * 1024;
-#pragma unroll
-                for (int j = 0; j < LA; ++j)
-                    if (8 * j + wave < 4 * RT) dma16(asrc, st + j * 8192, aoff[j], kt * FF_ROW);
+            auto read_x = [&](auto b_c, auto i_c, int kt) {
+                constexpr int B = decltype(b_c)::value, I = decltype(i_c)::value;
+                const uint32_t ab = FF_A0 + (uint32_t)(kt & 1) * FF_A + G * 16 * FF_ROW;
+                x[B][0] = ds_read16<I * 32 * (int)FF_ROW>(ab + fo[0]);
+                x[B][1] = ds_read16<I * 32 * (int)FF_ROW>(ab + fo[1]);
             };
-            auto run = [&](auto rg_c) {
-                constexpr int RG = decltype(rg_c)::value;            // row tiles of this wave
-                constexpr int RA = RG > 0 ? RG : 1;
-                f32x16 acc[RA][2];
-#pragma unroll
-                for (int i = 0; i < RA; ++i)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) acc[i][c] = f32x16{};
+            auto read_s = [&](int kt) {                            // three reads
+                const uint32_t sb = sbase + FF_S0 + (uint32_t)(kt & 1) * FF_S;
+                sx0 = ds_read16<0>(sb + (16 * G + m) * 32);
+                sx1 = ds_read8(sb + (16 * G + m) * 32 + 16);
+                swv = ds_read8(sb + 1024 + (PHASE == 2 ? (q >> 1) * 8 : 0));
+            };
+            auto tie_x = [&](auto b_c) {
+                tie_after_wait(x[decltype(b_c)::value][0]);
+                tie_after_wait(x[decltype(b_c)::value][1]);
+            };
+            auto tie_s = [&]() {
+                tie_after_wait(sx0);
+                tie_after_wait(sx1);
+                tie_after_wait(swv);
+            };
 
-                issue_w(0, 0);
-                issue_a(0, 0);
-                if (KB > 1) issue_w(1, 1);
-                int wslot = 0, aslot = 0;
-                for (int kt = 0; kt < KB; ++kt) {
-                    const float s0 = sw0[kt], s1 = sw1[kt];
-                    if (kt + 1 < KB) vm_wait<4>(); else vm_wait<0>();    // all but the next stage's weights
-                    __builtin_amdgcn_sched_barrier(0);
-                    __builtin_amdgcn_s_barrier();
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (kt + 1 < KB) issue_a(kt + 1, aslot ^ 1);
-                    if (kt + 2 < KB) issue_w(kt + 2, wslot == 0 ? 2 : wslot - 1);
-                    if constexpr (RG > 0) {
-                        const uint32_t wb = sbase + wslot * FF_W + wfo;
-                        const uint32_t ab = sbase + FF_A0 + aslot * FF_A + G * 32 * FF_ROW;
-                        const uint32_t sb = sbase + FF_S0 + aslot * 1024 + (32 * G + m) * 4;
-                        u32x4 w[2][2][2], x[2][2][2];                // [column tile][half][16 B], [buffer][half][16 B]
-                        uint32_t sx[RA];
-                        static_for<2>([&](auto h_c) {
-                            static_for<2>([&](auto j_c) {
-                                constexpr int Hh = decltype(h_c)::value, J = decltype(j_c)::value;
-                                w[0][Hh][J] = ds_read16<0>(wb + fo[Hh][J]);
-                                x[0][Hh][J] = ds_read16<0>(ab + fo[Hh][J]);
-                                w[1][Hh][J] = ds_read16<WC>(wb + fo[Hh][J]);
-                            });
-                        });
-#pragma unroll
-                        for (int i = 0; i < RG; ++i) sx[i] = ds_read4(sb + i * 256);
-                        lds_wait_all();
-                        static_for<2>([&](auto h_c) {
-                            static_for<2>([&](auto j_c) {
-                                constexpr int Hh = decltype(h_c)::value, J = decltype(j_c)::value;
-                                tie_after_wait(w[0][Hh][J]);
-                                tie_after_wait(w[1][Hh][J]);
-                                tie_after_wait(x[0][Hh][J]);
-                            });
-                        });
-#pragma unroll
-                        for (int i = 0; i < RG; ++i) tie_after_wait(sx[i]);
-                        static_for<RG>([&](auto i_c) {
-                            constexpr int I = decltype(i_c)::value, B = I & 1;
-                            if constexpr (I + 1 < RG) {
-                                static_for<2>([&](auto h_c) {
-                                    static_for<2>([&](auto j_c) {
-                                        constexpr int Hh = decltype(h_c)::value, J = decltype(j_c)::value;
-                                        x[B ^ 1][Hh][J] = ds_read16<(I + 1) * 64 * (int)FF_ROW>(ab + fo[Hh][J]);
-                                    });
-                                });
-                            }
-                            f32x16 p0 = mfma_fp8(pack8(w[0][0][0], w[0][0][1]), pack8(x[B][0][0], x[B][0][1]), f32x16{});
-                            f32x16 p1 = mfma_fp8(pack8(w[1][0][0], w[1][0][1]), pack8(x[B][0][0], x[B][0][1]), f32x16{});
-                            p0 = mfma_fp8(pack8(w[0][1][0], w[0][1][1]), pack8(x[B][1][0], x[B][1][1]), p0);
-                            p1 = mfma_fp8(pack8(w[1][1][0], w[1][1][1]), pack8(x[B][1][0], x[B][1][1]), p1);
-                            const float f0 = __uint_as_float(sx[I]) * s0;
-                            const float f1 = PHASE == 1 ? __uint_as_float(sx[I]) * s1 : f0;
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) acc[I][0][r] = fmaf(p0[r], f0, acc[I][0][r]);
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) acc[I][1][r] = fmaf(p1[r], f1, acc[I][1][r]);
-                            if constexpr (I + 1 < RG) {
-                                lds_wait_all();
-                                static_for<2>([&](auto h_c) {
-                                    static_for<2>([&](auto j_c) {
-                                        tie_after_wait(x[B ^ 1][decltype(h_c)::value][decltype(j_c)::value]);
-                                    });
-                                });
-                            }
-                        });
+            // One stage.  LDS returns in
+            // order, so a wait for all but the N newest reads is a wait for
+            // the older ones.  Reads run two tiles ahead: at tile t those of
+            // tile t + 2; before the last tile but one every wave has all
+            // rows of this stage (barrier: the rows, and the weights read in
+            // the stage before, make room for loads of later stages), and
+            // from there on the next stage's first two tiles, its scales and,
+            // behind the products that used the old ones, its weights (past the
+            // last stage: whatever lies there, unused).
+            auto stage = [&](int kt) {
+                const bool more = kt + 1 < KB;
+                auto boundary = [&]() {
+                    // the rows of stage kt + 1 and the weights of stage kt + 1: all but the newest weights
+                    if (kt + 2 < KB) vm_wait<4>(); else vm_wait<0>();
+                    barrier();
+                };
+                // Loads go out one at a time between the products (a burst of
+                // them holds up the wave at its issue): the weights of stage
+                // kt + 2 before the boundary, in the slot that stage kt - 1
+                // read, and behind it the rows and scales of stage kt + 2.
+                constexpr int WT = RG > 3 ? RG - 2 : 1;                    // tiles that the weight loads are spread over
+                auto weights = [&](int i) {
+                    if (kt + 2 < KB) issue_w(kt + 2, i);
+                };
+                auto rows = [&](int i) {
+                    if (kt + 2 < KB) {
+                        issue_a(kt + 2, i);
+                        if (i == 3) issue_s(kt + 2);
                     }
-                    wslot = wslot == 2 ? 0 : wslot + 1;
-                    aslot ^= 1;
-                }
-                __syncthreads();                                     // the ring becomes the staging tile
-
-                // result element r of lane (m, g): row 32 i + m, column 8 (r / 4) + 4 g + r % 4 of the column tile
-                constexpr uint32_t PITCH = ff_pitch<PHASE>();
-                uint32_t e0 = (uint32_t)(32 * G + m) * PITCH;
-                asm volatile("" : "+v"(e0));                         // (addresses derived here, not kept over the items)
-                if constexpr (PHASE == 1) {
-                    float* top = reinterpret_cast<float*>(lds + FP8_BM * PITCH);      // [4][256] row maxima by q
-                    float s[RA];
-                    static_for<RG>([&](auto i_c) {
-                        constexpr int I = decltype(i_c)::value;
-                        float tp = 0.0f;
+                };
+                static_for<RG>([&](auto t_c) {
+                    constexpr int I = decltype(t_c)::value, B = I % NB;
+                    constexpr bool LAST = I + 1 == RG;
+                    constexpr auto B2 = std::integral_constant<int, (I + 2) % NB>{};
+                    constexpr auto B1 = std::integral_constant<int, (I + 1) % NB>{};
+                    if constexpr (RG <= 2 && I == 0) static_for<4>([&](auto j_c) { weights(decltype(j_c)::value); });
+                    if constexpr (I + 2 == RG) {
+                        lds_wait_all();
+                        if constexpr (I == 0)
+                            static_for<4>([&](auto c_c) {
+                                tie_after_wait(w[decltype(c_c)::value][0]);
+                                tie_after_wait(w[decltype(c_c)::value][1]);
+                            });
+                        tie_x(std::integral_constant<int, B>{});
+                        tie_x(B1);
+                        if constexpr (I == 0) tie_s();
+                        if (more) boundary();
+                        if constexpr (RG > 2) read_x(B2, std::integral_constant<int, 0>{}, kt + 1);
+                    }
+                    if constexpr (LAST && RG > 2) read_x(B2, std::integral_constant<int, 1>{}, kt + 1);
+                    constexpr int O = (I + RG - 1) % RG;           // the tile whose partial sums are in p
+                    static_for<4>([&](auto c_c) {
+                        constexpr int C = decltype(c_c)::value;
+                        if constexpr (I == 0 && RG != 2) {
+                            // (the next column tiles' weights and the scales may still be on their way)
+                            asm volatile("s_waitcnt lgkmcnt(%0)" : : "n"(9 - 2 * C) : "memory");
+                            tie_after_wait(w[C][0]);
+                            tie_after_wait(w[C][1]);
+                            if constexpr (C == 0) {
+                                tie_x(std::integral_constant<int, B>{});
+                                if constexpr (RG > 1) tie_x(B1);
+                            }
+                        }
+                        const i32x8 xv = pack8(x[B][0], x[B][1]);
+                        __builtin_amdgcn_sched_barrier(0);
+                        const float f = PHASE == 1 && C >= 2 ? f1 : f0;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const float v = silu_mul(acc[I][0][r], acc[I][1][r]);
-                            acc[I][0][r] = v;
+                        for (int r = 0; r < 4; ++r) acc[O][C][r] = fmaf(p[C][r], f, acc[O][C][r]);
+                        asm volatile("" : "+v"(acc[O][C]));        // (here, not sunk to the end of the stage)
+                        __builtin_amdgcn_sched_barrier(0);
+                        p[C] = mfma16_fp8(pack8(w[C][0], w[C][1]), xv, f32x4{});
+                        __builtin_amdgcn_sched_barrier(0);
+                        if constexpr (RG > 2 && I < WT && C == 1)
+                            static_for<4 * (I + 1) / WT - 4 * I / WT>(
+                                [&](auto j_c) { weights(4 * I / WT + decltype(j_c)::value); });
+                        if constexpr (LAST && RG > 1) {
+                            read_w(c_c, kt + 1);
+                            rows(C);
+                        }
+                    });
+                    if constexpr (I + 2 < RG) read_x(B2, std::integral_constant<int, I + 2>{}, kt);
+                    if constexpr (RG == 2) read_x(std::integral_constant<int, B>{}, std::integral_constant<int, I>{}, kt + 1);
+                    if constexpr (I == 0 && RG != 2) {             // the stage's scales (and with them the next tile)
+                        asm volatile("s_waitcnt lgkmcnt(%0)" : : "n"(RG > 2 ? 2 : 0) : "memory");
+                        tie_s();
+                    } else if constexpr (I + 3 < RG) {             // (the last two tiles wait before the barrier)
+                        asm volatile("s_waitcnt lgkmcnt(2)" ::: "memory");
+                        tie_x(B1);
+                    }
+                    const uint32_t sr = I < 4 ? sx0[I & 3] : sx1[I & 1];
+                    f0 = __uint_as_float(sr) * __uint_as_float(swv[0]);
+                    f1 = PHASE == 1 ? __uint_as_float(sr) * __uint_as_float(swv[1]) : f0;
+                    if constexpr (LAST && RG > 1) read_s(kt + 1);
+                    if constexpr (RG == 1) {                       // a single tile: everything of the next stage behind the barrier
+                        if (more) {
+                            boundary();
+                            static_for<4>([&](auto j_c) { rows(decltype(j_c)::value); });
+                        }
+                        read_x(B1, std::integral_constant<int, 0>{}, kt + 1);
+                        static_for<4>([&](auto c_c) { read_w(c_c, kt + 1); });
+                        read_s(kt + 1);
+                    }
+                });
+                if constexpr (RG == 0) {
+                    static_for<4>([&](auto j_c) { weights(decltype(j_c)::value); });
+                    if (more) {
+                        boundary();
+                        static_for<4>([&](auto j_c) { rows(decltype(j_c)::value); });
+                    }
+                }
+            };
+
+            static_for<4>([&](auto j_c) { issue_w(0, decltype(j_c)::value); });
+            static_for<4>([&](auto j_c) { issue_a(0, decltype(j_c)::value); });
+            issue_s(0);
+            vm_wait<0>();
+            barrier();
+            if (KB > 1) {
+                static_for<4>([&](auto j_c) { issue_w(1, decltype(j_c)::value); });
+                static_for<4>([&](auto j_c) { issue_a(1, decltype(j_c)::value); });
+                issue_s(1);
+            }
+            if constexpr (RG > 0) {
+                read_x(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, 0);
+                if constexpr (RG > 1) read_x(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, 0);
+                static_for<4>([&](auto c_c) { read_w(c_c, 0); });
+                read_s(0);
+            }
+            int kt = 0;
+            do stage(kt); while (++kt < KB);
+            if constexpr (RG > 0) {
+                // the last stage's reads ahead hold nothing; they land before
+                // their registers are used again
+                lds_wait_all();
+                static_for<4>([&](auto c_c) {
+                    tie_after_wait(w[decltype(c_c)::value][0]);
+                    tie_after_wait(w[decltype(c_c)::value][1]);
+                });
+                static_for<NB>([&](auto b_c) { tie_x(b_c); });
+                tie_s();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[RA - 1][c][r] = fmaf(p[c][r], PHASE == 1 && c >= 2 ? f1 : f0, acc[RA - 1][c][r]);
+            }
+
+            // Result element i of tile t, column tile c: row 16 (2 t + G) + m, column 16 c + 4 kg + i
+            if constexpr (PHASE == 1) {
+                float* top = reinterpret_cast<float*>(lds + FF_T0);
+                static_for<RG>([&](auto t_c) {
+                    constexpr int I = decltype(t_c)::value;
+                    float tp = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float v = silu_mul(acc[I][c][r], acc[I][c + 2][r]);
+                            acc[I][c][r] = v;
                             tp = fmaxf(tp, finite_abs(v));
                         }
-                        tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
-                        if (g == 0) top[q * 256 + 64 * I + 32 * G + m] = tp;
-                    });
-                    __syncthreads();
-                    static_for<RG>([&](auto i_c) {
-                        constexpr int I = decltype(i_c)::value;
-                        const float* tr = top + 64 * I + 32 * G + m;
-                        s[I] = fp8_scale(fmaxf(fmaxf(tr[0], tr[256]), fmaxf(tr[512], tr[768])));
-                        const float rs = pow2_rcp(s[I]);
+                    tp = fmaxf(tp, __shfl_xor(tp, 16, 64));
+                    tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
+                    if (kg == 0) top[q * 256 + 32 * I + 16 * G + m] = tp;
+                });
+                __syncthreads();
+                static_for<RG>([&](auto t_c) {
+                    constexpr int I = decltype(t_c)::value;
+                    const int r = 32 * I + 16 * G + m;
+                    const float* tr = top + r;
+                    const float s = fp8_scale(fmaxf(fmaxf(tr[0], tr[256]), fmaxf(tr[512], tr[768])));
+                    const float rs = pow2_rcp(s);
+                    uint32_t v[2];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            *reinterpret_cast<uint32_t*>(lds + e0 + I * 64 * PITCH + 32 * q + 8 * c + 4 * g) =
-                                fp8_pack4(acc[I][0][4 * c] * rs, acc[I][0][4 * c + 1] * rs, acc[I][0][4 * c + 2] * rs,
-                                          acc[I][0][4 * c + 3] * rs);
-                        const int row = 64 * I + 32 * G + m;
-                        if (q == 0 && g == 0 && row < t.rows) a.as[(size_t)nt * P + t.row0 + row] = s[I];
-                    });
-                } else {
-                    static_for<RG>([&](auto i_c) {
-                        constexpr int I = decltype(i_c)::value;
+                    for (int c = 0; c < 2; ++c)
+                        v[c] = fp8_pack4(acc[I][c][0] * rs, acc[I][c][1] * rs, acc[I][c][2] * rs, acc[I][c][3] * rs);
+                    swap16(v[0], v[1]);                    // even kg: 8 columns of tile 0, odd kg: of tile 1
+                    if (r < t.rows) {
+                        *reinterpret_cast<uint2*>(a.act + (size_t)(t.row0 + r) * a.I + nt * 128 + 32 * q + 16 * (kg & 1) +
+                                                  4 * (kg & 2)) = make_uint2(v[0], v[1]);
+                        if (q == 0 && kg == 0) a.as[(size_t)nt * P + t.row0 + r] = s;
+                    }
+                });
+            } else {
+                static_for<RG>([&](auto t_c) {
+                    constexpr int I = decltype(t_c)::value;
+                    const int r = 32 * I + 16 * G + m;
+                    // 4 columns of each column tile per lane -> the 16 of tile kg
+                    uint32_t v[4][2];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const f32x16& v = acc[I][c];
-                                const uint32_t lo = (uint32_t)f32_to_f16_bits(v[4 * j]) |
-                                                    ((uint32_t)f32_to_f16_bits(v[4 * j + 1]) << 16);
-                                const uint32_t hi = (uint32_t)f32_to_f16_bits(v[4 * j + 2]) |
-                                                    ((uint32_t)f32_to_f16_bits(v[4 * j + 3]) << 16);
-                                *reinterpret_cast<uint2*>(lds + e0 + I * 64 * PITCH + (64 * q + 32 * c + 8 * j + 4 * g) * 2) =
-                                    make_uint2(lo, hi);
-                            }
-                    });
-                }
-            };
-            if (G == 0) run(std::integral_constant<int, (RT + 1) / 2>{});
-            else run(std::integral_constant<int, RT / 2>{});
+                        for (int h = 0; h < 2; ++h)
+                            v[c][h] = (uint32_t)f32_to_f16_bits(acc[I][c][2 * h]) |
+                                      ((uint32_t)f32_to_f16_bits(acc[I][c][2 * h + 1]) << 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        swap32(v[0][h], v[2][h]);
+                        swap32(v[1][h], v[3][h]);
+                        swap16(v[0][h], v[1][h]);
+                        swap16(v[2][h], v[3][h]);
+                    }
+                    if (r < t.rows) {
+                        uint16_t* dst = a.y + (size_t)(t.row0 + r) * a.H + nt * 256 + 64 * q + 16 * kg;
+                        stg16(dst, u32x4{v[0][0], v[0][1], v[1][0], v[1][1]});
+                        stg16(dst + 8, u32x4{v[2][0], v[2][1], v[3][0], v[3][1]});
+                    }
+                });
+            }
         };
-        switch (rt) {
-            case 7: kloop(std::integral_constant<int, 7>{}); break;
-            case 6: kloop(std::integral_constant<int, 6>{}); break;
-            case 5: kloop(std::integral_constant<int, 5>{}); break;
-            case 4: kloop(std::integral_constant<int, 4>{}); break;
-            case 3: kloop(std::integral_constant<int, 3>{}); break;
-            case 2: kloop(std::integral_constant<int, 2>{}); break;
-            default: kloop(std::integral_constant<int, 1>{}); break;
+        switch ((tt + 1 - G) >> 1) {
+            case 6: run(std::integral_constant<int, 6>{}); break;
+            case 5: run(std::integral_constant<int, 5>{}); break;
+            case 4: run(std::integral_constant<int, 4>{}); break;
+            case 3: run(std::integral_constant<int, 3>{}); break;
+            case 2: run(std::integral_constant<int, 2>{}); break;
+            case 1: run(std::integral_constant<int, 1>{}); break;
+            default: run(std::integral_constant<int, 0>{}); break;
         }
-        __syncthreads();
-        {
-            constexpr uint32_t PITCH = ff_pitch<PHASE>();
-            constexpr int BYTES = PHASE == 1 ? 128 : 512;            // of one output row
-            constexpr int CPR = BYTES / 16, RPP = FF_THREADS / CPR;
-            uint8_t* dst = PHASE == 1 ? a.act : reinterpret_cast<uint8_t*>(a.y);
-            const size_t ld = PHASE == 1 ? (size_t)a.I : (size_t)a.H * 2;
-            const int ch = tid % CPR;
-            for (int r = tid / CPR; r < t.rows; r += RPP)
-                stg16(dst + (size_t)(t.row0 + r) * ld + nt * BYTES + ch * 16,
-                      *reinterpret_cast<const u32x4*>(lds + r * PITCH + ch * 16));
-        }
-        __syncthreads();                                             // staging read before the next item's loads
+        __syncthreads();                                           // the ring and the maxima are free again
     }
 }
 

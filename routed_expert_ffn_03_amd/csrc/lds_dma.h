@@ -11,6 +11,8 @@
 
 namespace moe {
 
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
 // Raw buffer resource over [base, base + bytes): loads past the end return
 // zeros instead of touching memory.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
@@ -44,12 +46,19 @@ __device__ __forceinline__ uint32_t ds_read4(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ u32x2 ds_read8(uint32_t addr) {
+    u32x2 v;
+    asm volatile("ds_read_b64 %0, %1" : "=v"(v) : "v"(addr));
+    return v;
+}
+
 // Wait for all of this wave's LDS reads; then tie each destination register
 // to a point after the wait (an empty asm that "modifies" it), so that no use
 // of it is scheduled before the wait.
 __device__ __forceinline__ void lds_wait_all() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ void tie_after_wait(u32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void tie_after_wait(u32x2& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void tie_after_wait(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // Workgroup barrier for data exchanged through LDS only: waits for this
