@@ -96,59 +96,93 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     const uint32_t wfo = (uint32_t)(PHASE == 1 ? 32 * q : 64 * q) * FF_ROW;
     constexpr int WC2 = (PHASE == 1 ? 128 : 32) * (int)FF_ROW;
 
-    for (int item = logical_block(); item < n_items; item += gridDim.x) {
-        MTile t;
-        int nt;
-        fat_item(a.fat, item, NT, t, nt);
-        const int tt = (t.rows + 15) >> 4;                         // 16-row tiles
+    int item = logical_block();
+    if (item >= n_items) return;                                   // the whole block
+    MTile t;
+    int nt;
+    fat_item(a.fat, item, NT, t, nt);
+
+    // Where the loads of an item come from: set up for the item that is
+    // loaded next, which is the block's next item once the current one has
+    // all its stages under way.
+    __amdgpu_buffer_rsrc_t wsrc;
+    uint32_t aoff[3], woff[4];
+    int na;                                                        // activation instructions of the block per stage
+    const float* sp;
+    const size_t sstep = wave < 4 ? P : 1;
+    auto aim = [&](const MTile& u, int un) {
         const uint8_t* wmat = PHASE == 1 ? (wave < 4 ? a.wg : a.wu) : a.wd;
-        const __amdgpu_buffer_rsrc_t wsrc = make_rsrc(wmat + (size_t)t.e * wbytes, (uint32_t)wbytes);
+        wsrc = make_rsrc(wmat + (size_t)u.e * wbytes, (uint32_t)wbytes);
+        na = 2 * ((u.rows + 15) >> 4);
         // activation instruction j of this wave: tile rows 8 (8 j + wave) + L / 8 (rows past the M-tile repeat
         // its last one); weight instruction j: rows 32 wave + 8 j + L / 8 of the slot
-        uint32_t aoff[4], woff[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 3; ++j) {
             const int r = 8 * (8 * j + wave) + lr;
-            const int row = t.row0 + min(r, t.rows - 1);
+            const int row = u.row0 + min(r, u.rows - 1);
             const uint32_t src = PHASE == 1 ? (uint32_t)(a.sorted_pair[row] / a.k) : (uint32_t)row;
             aoff[j] = src * (uint32_t)K + piece(r);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             const int w = 32 * wave + 8 * j + lr;
-            const uint32_t wrow = PHASE == 1 ? (uint32_t)(nt * 128 + (w & 127)) : (uint32_t)(nt * 256 + w);
+            const uint32_t wrow = PHASE == 1 ? (uint32_t)(un * 128 + (w & 127)) : (uint32_t)(un * 256 + w);
             woff[j] = wrow * (uint32_t)K + piece(w);
         }
-        const int na = 2 * tt;                                     // activation instructions of the block per stage
-        // Scales of stage kt, 4 bytes per lane: waves 0-3 the row scales, 64
+        // Scales of a stage, 4 bytes per lane: waves 0-3 the row scales, 64
         // each, from the block-major array (position 8 (16 G + m) + t holds
         // row 32 t + 16 G + m, so that a lane finds its tiles' scales in a
         // row); wave 4 the two block scales of W (phase 1: gate, up; phase 2:
         // those of the lower and, 8 bytes on, of the upper 128 columns)
-        const float* sp;
-        size_t sstep;
-        {
-            const int pos = 64 * q + lane, r = 32 * (pos & 7) + (pos >> 3);
-            const float* rows = (PHASE == 1 ? a.xst : a.as) + t.row0 + min(r, t.rows - 1);
-            const size_t soff = (size_t)t.e * (N / FP8_BLOCK) * KB;
-            const float* blocks = PHASE == 1 ? (lane == 0 ? a.sg : a.su) + soff + (size_t)nt * KB
-                                             : a.sd + soff + (size_t)(2 * nt + (lane < 2 ? 0 : 1)) * KB;
-            sp = wave < 4 ? rows : blocks;
-            sstep = wave < 4 ? P : 1;
-        }
-        auto issue_w = [&](int kt, int j) {                        // weight instruction j of stage kt
-            dma16(wsrc, lds + (kt % FF_NW) * FF_W + wave * 4096 + j * 1024, woff[j], kt * FF_ROW);
-        };
-        auto issue_a = [&](int kt, int j) {                        // activation instruction j, if the M-tile has its rows
-            if (8 * j + wave < na) dma16(asrc, lds + FF_A0 + (kt & 1) * FF_A + wave * 1024 + j * 8192, aoff[j], kt * FF_ROW);
-        };
-        auto issue_s = [&](int kt) {
-            if (wave < 5)
-                __builtin_amdgcn_global_load_lds((gptr_t)(sp + kt * sstep),
-                                                 (lds_ptr_t)(lds + FF_S0 + (kt & 1) * FF_S + wave * 256), 4, 0, 0);
-        };
-        auto barrier = [&]() {
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        };
+        const int pos = 64 * q + lane, r = 32 * (pos & 7) + (pos >> 3);
+        const float* rows = (PHASE == 1 ? a.xst : a.as) + u.row0 + min(r, u.rows - 1);
+        const size_t soff = (size_t)u.e * (N / FP8_BLOCK) * KB;
+        const float* blocks = PHASE == 1 ? (lane == 0 ? a.sg : a.su) + soff + (size_t)un * KB
+                                         : a.sd + soff + (size_t)(2 * un + (lane < 2 ? 0 : 1)) * KB;
+        sp = wave < 4 ? rows : blocks;
+    };
+    // slots of stage 0 of the current item: the stages of all items go round
+    int w0 = 0, a0 = 0;
+    auto wslot = [&](int kt) { return (uint32_t)(w0 + kt) % FF_NW; };
+    auto aslot = [&](int kt) { return (uint32_t)(a0 + kt) & 1; };
+    auto issue_w = [&](int kt, int j) {                            // weight instruction j of stage kt
+        dma16(wsrc, lds + wslot(kt) * FF_W + wave * 4096 + j * 1024, woff[j], kt * FF_ROW);
+    };
+    auto issue_a = [&](int kt, int j) {                            // activation instruction j, if the M-tile has its rows
+        if (8 * j + wave < na) dma16(asrc, lds + FF_A0 + aslot(kt) * FF_A + wave * 1024 + j * 8192, aoff[j], kt * FF_ROW);
+    };
+    auto issue_s = [&](int kt) {
+        if (wave < 5)
+            __builtin_amdgcn_global_load_lds((gptr_t)(sp + kt * sstep),
+                                             (lds_ptr_t)(lds + FF_S0 + aslot(kt) * FF_S + wave * 256), 4, 0, 0);
+    };
+    auto issue_rows = [&](int kt) {
+        static_for<3>([&](auto j_c) { issue_a(kt, decltype(j_c)::value); });
+        issue_s(kt);
+    };
+    // the first loads of an item: weights of stages 0 and 1, rows of stage 0
+    auto issue_first = [&]() {
+        static_for<4>([&](auto j_c) { issue_w(0, decltype(j_c)::value); });
+        issue_rows(0);
+        if (KB > 1) static_for<4>([&](auto j_c) { issue_w(1, decltype(j_c)::value); });
+    };
+    auto barrier = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    aim(t, nt);
+    issue_first();
+    vm_wait<0>();
+    barrier();
+    for (;;) {
+        const int tt = (t.rows + 15) >> 4;                         // 16-row tiles
+        const bool has_next = item + (int)gridDim.x < n_items;
+        MTile tn;
+        int ntn;
+        fat_item(a.fat, has_next ? item + (int)gridDim.x : item, NT, tn, ntn);
+        if (KB > 1) issue_rows(1);
 
         auto run = [&](auto rg_c) {
             constexpr int RG = decltype(rg_c)::value;              // row tiles of this wave: G, G + 2, ...
@@ -169,18 +203,18 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             u32x2 sx1, swv;                                        // row scales of tiles 0-3 and 4, 5; block scales
             auto read_w = [&](auto c_c, int kt) {
                 constexpr int C = decltype(c_c)::value;
-                const uint32_t wb = (uint32_t)(kt % FF_NW) * FF_W + wfo;
+                const uint32_t wb = wslot(kt) * FF_W + wfo;
                 w[C][0] = ds_read16<(C & 1) * 16 * (int)FF_ROW + (C >> 1) * WC2>(wb + fo[0]);
                 w[C][1] = ds_read16<(C & 1) * 16 * (int)FF_ROW + (C >> 1) * WC2>(wb + fo[1]);
             };
             auto read_x = [&](auto b_c, auto i_c, int kt) {
                 constexpr int B = decltype(b_c)::value, I = decltype(i_c)::value;
-                const uint32_t ab = FF_A0 + (uint32_t)(kt & 1) * FF_A + G * 16 * FF_ROW;
+                const uint32_t ab = FF_A0 + aslot(kt) * FF_A + G * 16 * FF_ROW;
                 x[B][0] = ds_read16<I * 32 * (int)FF_ROW>(ab + fo[0]);
                 x[B][1] = ds_read16<I * 32 * (int)FF_ROW>(ab + fo[1]);
             };
             auto read_s = [&](int kt) {                            // three reads
-                const uint32_t sb = sbase + FF_S0 + (uint32_t)(kt & 1) * FF_S;
+                const uint32_t sb = sbase + FF_S0 + aslot(kt) * FF_S;
                 sx0 = ds_read16<0>(sb + (16 * G + m) * 32);
                 sx1 = ds_read8(sb + (16 * G + m) * 32 + 16);
                 swv = ds_read8(sb + 1024 + (PHASE == 2 ? (q >> 1) * 8 : 0));
@@ -221,8 +255,8 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 };
                 auto rows = [&](int i) {
                     if (kt + 2 < KB) {
-                        issue_a(kt + 2, i);
-                        if (i == 3) issue_s(kt + 2);
+                        if (i < 3) issue_a(kt + 2, i);
+                        else issue_s(kt + 2);
                     }
                 };
                 static_for<RG>([&](auto t_c) {
@@ -307,16 +341,6 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 }
             };
 
-            static_for<4>([&](auto j_c) { issue_w(0, decltype(j_c)::value); });
-            static_for<4>([&](auto j_c) { issue_a(0, decltype(j_c)::value); });
-            issue_s(0);
-            vm_wait<0>();
-            barrier();
-            if (KB > 1) {
-                static_for<4>([&](auto j_c) { issue_w(1, decltype(j_c)::value); });
-                static_for<4>([&](auto j_c) { issue_a(1, decltype(j_c)::value); });
-                issue_s(1);
-            }
             if constexpr (RG > 0) {
                 read_x(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, 0);
                 if constexpr (RG > 1) read_x(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, 0);
@@ -341,6 +365,16 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                     for (int r = 0; r < 4; ++r) acc[RA - 1][c][r] = fmaf(p[c][r], PHASE == 1 && c >= 2 ? f1 : f0, acc[RA - 1][c][r]);
             }
 
+            // The next item's first loads go out here, into slots that no
+            // wave reads any more (its stage 0 follows this item's last one),
+            // and land over the epilogue.
+            if (has_next) {
+                aim(tn, ntn);
+                w0 = (w0 + KB) % FF_NW;
+                a0 = (a0 + KB) & 1;
+                issue_first();
+            }
+
             // Result element i of tile t, column tile c: row 16 (2 t + G) + m, column 16 c + 4 kg + i
             if constexpr (PHASE == 1) {
                 float* top = reinterpret_cast<float*>(lds + FF_T0);
@@ -359,7 +393,8 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                     tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
                     if (kg == 0) top[q * 256 + 32 * I + 16 * G + m] = tp;
                 });
-                __syncthreads();
+                vm_wait<0>();                                      // the next item's loads; the stores below stay behind
+                lds_barrier();
                 static_for<RG>([&](auto t_c) {
                     constexpr int I = decltype(t_c)::value;
                     const int r = 32 * I + 16 * G + m;
@@ -378,6 +413,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                     }
                 });
             } else {
+                vm_wait<0>();
                 static_for<RG>([&](auto t_c) {
                     constexpr int I = decltype(t_c)::value;
                     const int r = 32 * I + 16 * G + m;
@@ -413,7 +449,11 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             case 1: run(std::integral_constant<int, 1>{}); break;
             default: run(std::integral_constant<int, 0>{}); break;
         }
-        __syncthreads();                                           // the ring and the maxima are free again
+        lds_barrier();                                             // everybody's loads have landed; the maxima are free again
+        if (!has_next) break;
+        item += gridDim.x;
+        t = tn;
+        nt = ntn;
     }
 }
 
