@@ -72,9 +72,9 @@ __device__ __forceinline__ int logical_block() {
 // 32 consecutive items that the blocks of one XCD take at a time then cover s
 // activation tiles and about 32 / s weight tiles, each fetched once into that
 // XCD's L2 and shared.
-__device__ __forceinline__ void fat_item(const MTile* __restrict__ fat, int item, int NT, MTile& t, int& nt) {
-    const int q0 = item / NT;
-    const MTile t0 = fat[q0];
+// (fat_item_of: t0 = fat[item / NT] given, any M-tile of the item's expert.)
+__device__ __forceinline__ void fat_item_of(const MTile* __restrict__ fat, const MTile& t0, int item, int NT, MTile& t,
+                                            int& nt) {
     const int me = t0.count, local = item - t0.first * NT;
     const int nblk = (me + 7) >> 3;
     const int q = me / nblk, r = me - q * nblk;              // r blocks of q + 1 M-tiles, then blocks of q
@@ -89,6 +89,10 @@ __device__ __forceinline__ void fat_item(const MTile* __restrict__ fat, int item
     }
     nt = off / s;
     t = fat[t0.first + m0 + (off - nt * s)];
+}
+
+__device__ __forceinline__ void fat_item(const MTile* __restrict__ fat, int item, int NT, MTile& t, int& nt) {
+    fat_item_of(fat, fat[item / NT], item, NT, t, nt);
 }
 
 // The M-tiles of expert e (route list rows [r0, r0 + n)): nf fat tiles from

@@ -98,9 +98,11 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
 
     int item = logical_block();
     if (item >= n_items) return;                                   // the whole block
-    MTile t;
-    int nt;
+    MTile t, tn;                                                   // this item's M-tile and the next one's
+    int nt, ntn;
+    const int second = min(item + (int)gridDim.x, n_items - 1);
     fat_item(a.fat, item, NT, t, nt);
+    fat_item(a.fat, second, NT, tn, ntn);
 
     // Where the loads of an item come from: set up for the item that is
     // loaded next, which is the block's next item once the current one has
@@ -110,7 +112,15 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     int na;                                                        // activation instructions of the block per stage
     const float* sp;
     const size_t sstep = wave < 4 ? P : 1;
-    auto aim = [&](const MTile& u, int un) {
+    // the route-list entries of an M-tile's rows that this lane loads
+    auto entries = [&](const MTile& u, int (&en)[3]) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int row = u.row0 + min(8 * (8 * j + wave) + lr, u.rows - 1);
+            en[j] = PHASE == 1 ? a.sorted_pair[row] : row;
+        }
+    };
+    auto aim = [&](const MTile& u, int un, const int (&en)[3]) {
         const uint8_t* wmat = PHASE == 1 ? (wave < 4 ? a.wg : a.wu) : a.wd;
         wsrc = make_rsrc(wmat + (size_t)u.e * wbytes, (uint32_t)wbytes);
         na = 2 * ((u.rows + 15) >> 4);
@@ -118,10 +128,8 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
         // its last one); weight instruction j: rows 32 wave + 8 j + L / 8 of the slot
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-            const int r = 8 * (8 * j + wave) + lr;
-            const int row = u.row0 + min(r, u.rows - 1);
-            const uint32_t src = PHASE == 1 ? (uint32_t)(a.sorted_pair[row] / a.k) : (uint32_t)row;
-            aoff[j] = src * (uint32_t)K + piece(r);
+            const uint32_t src = (uint32_t)(PHASE == 1 ? en[j] / a.k : en[j]);
+            aoff[j] = src * (uint32_t)K + piece(8 * (8 * j + wave) + lr);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -172,16 +180,23 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    aim(t, nt);
+    {
+        int en[3];
+        entries(t, en);
+        aim(t, nt, en);
+    }
     issue_first();
     vm_wait<0>();
     barrier();
     for (;;) {
         const int tt = (t.rows + 15) >> 4;                         // 16-row tiles
         const bool has_next = item + (int)gridDim.x < n_items;
-        MTile tn;
-        int ntn;
-        fat_item(a.fat, has_next ? item + (int)gridDim.x : item, NT, tn, ntn);
+        // ahead of the stages, used after them: the next item's route-list
+        // entries and the expert of the item after it
+        int en[3];
+        entries(tn, en);
+        const int ahead = min(item + 2 * (int)gridDim.x, n_items - 1);
+        const MTile tq = a.fat[ahead / NT];
         if (KB > 1) issue_rows(1);
 
         auto run = [&](auto rg_c) {
@@ -369,7 +384,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             // wave reads any more (its stage 0 follows this item's last one),
             // and land over the epilogue.
             if (has_next) {
-                aim(tn, ntn);
+                aim(tn, ntn, en);
                 w0 = (w0 + KB) % FF_NW;
                 a0 = (a0 + KB) & 1;
                 issue_first();
@@ -387,8 +402,15 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                         for (int r = 0; r < 4; ++r) {
                             const float v = silu_mul(acc[I][c][r], acc[I][c + 2][r]);
                             acc[I][c][r] = v;
-                            tp = fmaxf(tp, finite_abs(v));
+                            tp = fmaxf(tp, fabsf(v));              // (NaN is passed over)
                         }
+                    if (__builtin_expect(__any(tp == __uint_as_float(0x7f800000u)), 0)) {
+                        tp = 0.0f;                                 // an infinity somewhere: over the finite values
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) tp = fmaxf(tp, finite_abs(acc[I][c][r]));
+                    }
                     tp = fmaxf(tp, __shfl_xor(tp, 16, 64));
                     tp = fmaxf(tp, __shfl_xor(tp, 32, 64));
                     if (kg == 0) top[q * 256 + 32 * I + 16 * G + m] = tp;
@@ -454,6 +476,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
         item += gridDim.x;
         t = tn;
         nt = ntn;
+        fat_item_of(a.fat, tq, ahead, NT, tn, ntn);
     }
 }
 
