@@ -18,7 +18,7 @@
 namespace moe {
 
 constexpr int FP8_BLOCK = 128;
-constexpr int FP8_BM = 192;              // rows per MFMA M-tile: leaves LDS for the row scales (fp8_fat.hip)
+constexpr int FP8_BM = 224;              // rows per MFMA M-tile: leaves LDS for the row scales (fp8_fat.hip)
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 

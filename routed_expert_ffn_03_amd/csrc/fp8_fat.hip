@@ -47,7 +47,7 @@ constexpr uint32_t FF_S = 256 * 4 + 256;                   // scale slot: 256 ro
 constexpr uint32_t FF_T0 = FF_S0 + FF_NA * FF_S;           // row maxima of the four column groups
 constexpr uint32_t FF_LDS = FF_T0 + 4 * 256 * 4;
 static_assert(FF_LDS <= 160 * 1024, "LDS of one CU");
-static_assert(FP8_BM <= 192, "at most six 16-row tiles for a wave");
+static_assert(FP8_BM <= 224, "at most seven 16-row tiles for a wave");
 
 // Exchanges between lanes that differ in lane bit 5 (or 4): afterwards a lane
 // with that bit clear holds both lanes' a, one with it set both lanes' b (in
@@ -108,26 +108,26 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     // loaded next, which is the block's next item once the current one has
     // all its stages under way.
     __amdgpu_buffer_rsrc_t wsrc;
-    uint32_t aoff[3], woff[4];
+    uint32_t aoff[4], woff[4];
     int na;                                                        // activation instructions of the block per stage
     const float* sp;
     const size_t sstep = wave < 4 ? P : 1;
     // the route-list entries of an M-tile's rows that this lane loads
-    auto entries = [&](const MTile& u, int (&en)[3]) {
+    auto entries = [&](const MTile& u, int (&en)[4]) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const int row = u.row0 + min(8 * (8 * j + wave) + lr, u.rows - 1);
             en[j] = PHASE == 1 ? a.sorted_pair[row] : row;
         }
     };
-    auto aim = [&](const MTile& u, int un, const int (&en)[3]) {
+    auto aim = [&](const MTile& u, int un, const int (&en)[4]) {
         const uint8_t* wmat = PHASE == 1 ? (wave < 4 ? a.wg : a.wu) : a.wd;
         wsrc = make_rsrc(wmat + (size_t)u.e * wbytes, (uint32_t)wbytes);
         na = 2 * ((u.rows + 15) >> 4);
         // activation instruction j of this wave: tile rows 8 (8 j + wave) + L / 8 (rows past the M-tile repeat
         // its last one); weight instruction j: rows 32 wave + 8 j + L / 8 of the slot
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const uint32_t src = (uint32_t)(PHASE == 1 ? en[j] / a.k : en[j]);
             aoff[j] = src * (uint32_t)K + piece(8 * (8 * j + wave) + lr);
         }
@@ -165,7 +165,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                                              (lds_ptr_t)(lds + FF_S0 + aslot(kt) * FF_S + wave * 256), 4, 0, 0);
     };
     auto issue_rows = [&](int kt) {
-        static_for<3>([&](auto j_c) { issue_a(kt, decltype(j_c)::value); });
+        static_for<4>([&](auto j_c) { issue_a(kt, decltype(j_c)::value); });
         issue_s(kt);
     };
     // the first loads of an item: weights of stages 0 and 1, rows of stage 0
@@ -181,7 +181,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
     };
 
     {
-        int en[3];
+        int en[4];
         entries(t, en);
         aim(t, nt, en);
     }
@@ -193,7 +193,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
         const bool has_next = item + (int)gridDim.x < n_items;
         // ahead of the stages, used after them: the next item's route-list
         // entries and the expert of the item after it
-        int en[3];
+        int en[4];
         entries(tn, en);
         const int ahead = min(item + 2 * (int)gridDim.x, n_items - 1);
         const MTile tq = a.fat[ahead / NT];
@@ -202,10 +202,12 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
         auto run = [&](auto rg_c) {
             constexpr int RG = decltype(rg_c)::value;              // row tiles of this wave: G, G + 2, ...
             constexpr int RA = RG > 0 ? RG : 1;
-            // ring of row fragments: a divisor of RG, so that a tile has the
-            // same registers in every stage, and three at least where reads
-            // run two tiles ahead (RG > 2)
-            constexpr int NB = RG % 3 == 0 ? 3 : RA;
+            // Row fragments: tile i has the same registers in every stage,
+            // and any three consecutive tiles (around the stage's end too,
+            // where RG > 2) have different ones: 0 1 2, 0 1 2 3, 0 1 2 3 4,
+            // 0 1 2 0 1 2, 0 1 2 0 1 2 3.
+            constexpr int NB = RG % 3 == 0 ? 3 : RG == 7 ? 4 : RA;
+            constexpr auto buffer = [](int i) { return RG == 7 ? (i % 7 == 6 ? 3 : i % 7 % 3) : i % NB; };
             f32x4 acc[RA][4], p[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -214,8 +216,8 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 for (int i = 0; i < RA; ++i) acc[i][c] = f32x4{};
             }
             float f0 = 0.0f, f1 = 0.0f;                            // scales of the partial sums in p
-            u32x4 w[4][2], x[NB][2], sx0;                    // weights by column tile, rows in a ring of three tiles
-            u32x2 sx1, swv;                                        // row scales of tiles 0-3 and 4, 5; block scales
+            u32x4 w[4][2], x[NB][2], sx0, sx1;                    // weights by column tile, rows in a ring of three tiles
+            u32x2 swv;                                             // (sx0, sx1: row scales of tiles 0-3, 4-6) block scales
             auto read_w = [&](auto c_c, int kt) {
                 constexpr int C = decltype(c_c)::value;
                 const uint32_t wb = wslot(kt) * FF_W + wfo;
@@ -231,7 +233,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             auto read_s = [&](int kt) {                            // three reads
                 const uint32_t sb = sbase + FF_S0 + aslot(kt) * FF_S;
                 sx0 = ds_read16<0>(sb + (16 * G + m) * 32);
-                sx1 = ds_read8(sb + (16 * G + m) * 32 + 16);
+                sx1 = ds_read16<16>(sb + (16 * G + m) * 32);
                 swv = ds_read8(sb + 1024 + (PHASE == 2 ? (q >> 1) * 8 : 0));
             };
             auto tie_x = [&](auto b_c) {
@@ -270,15 +272,15 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 };
                 auto rows = [&](int i) {
                     if (kt + 2 < KB) {
-                        if (i < 3) issue_a(kt + 2, i);
-                        else issue_s(kt + 2);
+                        issue_a(kt + 2, i);
+                        if (i == 3) issue_s(kt + 2);
                     }
                 };
                 static_for<RG>([&](auto t_c) {
-                    constexpr int I = decltype(t_c)::value, B = I % NB;
+                    constexpr int I = decltype(t_c)::value, B = buffer(I);
                     constexpr bool LAST = I + 1 == RG;
-                    constexpr auto B2 = std::integral_constant<int, (I + 2) % NB>{};
-                    constexpr auto B1 = std::integral_constant<int, (I + 1) % NB>{};
+                    constexpr auto B2 = std::integral_constant<int, buffer(I + 2)>{};
+                    constexpr auto B1 = std::integral_constant<int, buffer(I + 1)>{};
                     if constexpr (RG <= 2 && I == 0) static_for<4>([&](auto j_c) { weights(decltype(j_c)::value); });
                     if constexpr (I + 2 == RG) {
                         lds_wait_all();
@@ -333,7 +335,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                         asm volatile("s_waitcnt lgkmcnt(2)" ::: "memory");
                         tie_x(B1);
                     }
-                    const uint32_t sr = I < 4 ? sx0[I & 3] : sx1[I & 1];
+                    const uint32_t sr = I < 4 ? sx0[I & 3] : sx1[I & 3];
                     f0 = __uint_as_float(sr) * __uint_as_float(swv[0]);
                     f1 = PHASE == 1 ? __uint_as_float(sr) * __uint_as_float(swv[1]) : f0;
                     if constexpr (LAST && RG > 1) read_s(kt + 1);
@@ -463,6 +465,7 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
             }
         };
         switch ((tt + 1 - G) >> 1) {
+            case 7: run(std::integral_constant<int, 7>{}); break;
             case 6: run(std::integral_constant<int, 6>{}); break;
             case 5: run(std::integral_constant<int, 5>{}); break;
             case 4: run(std::integral_constant<int, 4>{}); break;
