@@ -100,8 +100,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it, where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -116,44 +122,53 @@ def _dev(t: torch.Tensor, dtype, name: str):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor on the GPU")
 
 
-def _here(**tensors):
-    """Every given tensor lies on the current device, the one the launch and the default stream are on."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _shaped(t, dtype, name: str, shape):
-    _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+def _current(t, name: str) -> int:
+    """The current device's index, once ``t`` is known to be a GPU tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name}: expected a tensor on the GPU")
+    return torch.cuda.current_device()
 
 
-def _codes(t, name: str, shape):
-    """e4m3 codes: uint8 or float8_e4m3fn."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in (torch.uint8, torch.float8_e4m3fn)
+def _arg(t, name: str, dtypes, shape, dev: int):
+    """The address of a contiguous tensor of one of ``dtypes`` and of ``shape`` on device ``dev``, the current one
+    (the launch and the default stream are there)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
             and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous uint8 or float8_e4m3fn tensor on the GPU")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
+    raise ValueError(f"{name}: expected a contiguous tensor of {' or '.join(str(d) for d in dtypes)} and shape "
+                     f"{tuple(shape)} on the current device (cuda:{dev}), got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     + ("" if t.is_contiguous() else ", not contiguous"))
 
 
-def _fp8_experts(E, H, I, gate_up=None, down=None):
-    """Types and shapes of e4m3 expert weights and their fp32 scales per 128 x 128 block."""
+_F32, _I32, _U8, _F16 = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.float16, torch.int16)
+_BF16, _MASK = (torch.bfloat16, torch.int16), (torch.uint8, torch.bool)
+
+
+def _fp8_experts(E, H, I, gate_up=None, down=None, **others):
+    """Types and shapes of e4m3 expert weights and their fp32 scales per 128 x 128 block; they and the ``others``
+    lie on the current device."""
     if H % 128 or I % 128:
         raise ValueError(f"e4m3 experts: H = {H} and I = {I} must be multiples of 128")
     if gate_up is not None:
         w_gate, w_up, s_gate, s_up = gate_up
-        for w, sc, n in ((w_gate, s_gate, "gate"), (w_up, s_up, "up")):
-            _codes(w, f"w_{n}", (E, I, H))
-            _shaped(sc, torch.float32, f"s_{n}", (E, I // 128, H // 128))
-        _here(w_gate=w_gate, w_up=w_up, s_gate=s_gate, s_up=s_up)
+        dev = _current(w_gate, "w_gate")
+        _arg(w_gate, "w_gate", _CODES, (E, I, H), dev)
+        _arg(w_up, "w_up", _CODES, (E, I, H), dev)
+        _arg(s_gate, "s_gate", _F32, (E, I // 128, H // 128), dev)
+        _arg(s_up, "s_up", _F32, (E, I // 128, H // 128), dev)
     if down is not None:
         w_down, s_down = down
-        _codes(w_down, "w_down", (E, H, I))
-        _shaped(s_down, torch.float32, "s_down", (E, H // 128, I // 128))
-        _here(w_down=w_down, s_down=s_down)
+        dev = _current(w_down, "w_down")
+        _arg(w_down, "w_down", _CODES, (E, H, I), dev)
+        _arg(s_down, "s_down", _F32, (E, H // 128, I // 128), dev)
+    for name, t in others.items():
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
 def moe_workspace_size(T: int, E: int, k: int, H: int, I: int, wfmt: int = MOE_WFMT_BF16) -> int:
@@ -231,7 +246,8 @@ def moe_grouped_ffn(x, w_gate, w_up, w_down, expert_offsets, sorted_pair, k, y_s
     if tuple(y_sorted.shape) != (T * k, H):
         raise ValueError(f"y_sorted: shape {tuple(y_sorted.shape)} != {(T * k, H)}")
     if wfmt == MOE_WFMT_FP8_B128:
-        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down))
+        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down), x=x, y_sorted=y_sorted,
+                     expert_offsets=expert_offsets, sorted_pair=sorted_pair, workspace=workspace)
     _check(lib().moe_grouped_ffn(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate),
                                  _ptr(s_up), _ptr(s_down), _ptr(expert_offsets), _ptr(sorted_pair), T, E, k, H, I,
                                  fat_threshold, _ptr(y_sorted), _ptr(workspace), workspace.numel(),
@@ -276,7 +292,8 @@ def moe_grouped_ffn_noalloc(x, w_gate, w_up, w_down, expert_offsets, sorted_pair
     if tuple(y_sorted.shape) != (T * k, H):
         raise ValueError(f"y_sorted: shape {tuple(y_sorted.shape)} != {(T * k, H)}")
     if wfmt == MOE_WFMT_FP8_B128:
-        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down))
+        _fp8_experts(E, H, I, (w_gate, w_up, s_gate, s_up), (w_down, s_down), x=x, y_sorted=y_sorted,
+                     expert_offsets=expert_offsets, sorted_pair=sorted_pair)
     _check(lib().moe_grouped_ffn_noalloc(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(s_gate),
                                          _ptr(s_up), _ptr(s_down), _ptr(expert_offsets), _ptr(sorted_pair), T, E,
                                          k, H, I, fat_threshold, _ptr(y_sorted), _stream(stream)),
@@ -297,7 +314,7 @@ def moe_ffn_gate_up(x, w_gate, w_up, sorted_pair, E, k, workspace, s_gate=None, 
     T, H = x.shape
     I = w_gate.shape[1]
     if wfmt == MOE_WFMT_FP8_B128:
-        _fp8_experts(E, H, I, gate_up=(w_gate, w_up, s_gate, s_up))
+        _fp8_experts(E, H, I, gate_up=(w_gate, w_up, s_gate, s_up), x=x, sorted_pair=sorted_pair, workspace=workspace)
     _check(lib().moe_ffn_gate_up(_ptr(x), wfmt, _ptr(w_gate), _ptr(w_up), _ptr(s_gate), _ptr(s_up),
                                  _ptr(sorted_pair), T, E, k, H, I, fat_threshold, _ptr(workspace),
                                  workspace.numel(), _stream(stream)), "moe_ffn_gate_up")
@@ -307,7 +324,7 @@ def moe_ffn_down(w_down, T, E, k, I, y_sorted, workspace, s_down=None, fat_thres
                  wfmt=MOE_WFMT_BF16, stream=None):
     H = y_sorted.shape[1]
     if wfmt == MOE_WFMT_FP8_B128:
-        _fp8_experts(E, H, I, down=(w_down, s_down))
+        _fp8_experts(E, H, I, down=(w_down, s_down), y_sorted=y_sorted, workspace=workspace)
     _check(lib().moe_ffn_down(wfmt, _ptr(w_down), _ptr(s_down), T, E, k, H, I, fat_threshold, _ptr(y_sorted),
                               _ptr(workspace), workspace.numel(), _stream(stream)), "moe_ffn_down")
 
@@ -343,32 +360,32 @@ def moe_quantize_fp8(src, codes, scales, block_rows=1, stream=None):
     """e4m3 ``codes`` (uint8 or float8_e4m3fn, the shape of ``src``) and fp32 ``scales``
     [..., rows / block_rows, cols / 128] of bf16 ``src`` [..., rows, cols]; ``block_rows`` 1 for
     activations, 128 for the weights of ``MOE_WFMT_FP8_B128``."""
-    if not (isinstance(src, torch.Tensor) and src.is_cuda and src.dtype in (torch.bfloat16, torch.int16)
-            and src.is_contiguous()):
-        raise ValueError("src: expected a contiguous bfloat16 (or int16 bit pattern) tensor on the GPU")
-    if src.dim() < 2 or src.numel() == 0:
-        raise ValueError(f"src: shape {tuple(src.shape)}: [..., rows, cols] with at least one value expected")
+    dev = _current(src, "src")
+    shape = src.shape
+    n = src.numel()
+    if len(shape) < 2 or n == 0:
+        raise ValueError(f"src: shape {tuple(shape)}: [..., rows, cols] with at least one value expected")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows {block_rows}: 1 or 128")
-    rows, cols = int(src.shape[-2]), int(src.shape[-1])
+    rows, cols = shape[-2], shape[-1]
     if cols % 128 or rows % block_rows:
         raise ValueError(f"src: {rows} x {cols} is not a whole number of {block_rows} x 128 blocks")
-    _codes(codes, "codes", src.shape)
-    _shaped(scales, torch.float32, "scales", (*src.shape[:-2], rows // block_rows, cols // 128))
-    _here(src=src, codes=codes, scales=scales)
-    _check(lib().moe_quantize_fp8(_ptr(src), src.numel() // (rows * cols), rows, cols, block_rows, _ptr(codes),
-                                  _ptr(scales), _stream(stream)), "moe_quantize_fp8")
+    _check(lib().moe_quantize_fp8(
+        _arg(src, "src", _BF16, shape, dev), n // (rows * cols), rows, cols, block_rows,
+        _arg(codes, "codes", _CODES, shape, dev),
+        _arg(scales, "scales", _F32, (*shape[:-2], rows // block_rows, cols // 128), dev),
+        _stream(stream)), "moe_quantize_fp8")
 
 
 def moe_balance_workspace_size(T: int, E: int, groups: int = 1) -> int:
     return int(lib().moe_balance_workspace_size(T, E, groups))
 
 
-def _token_mask(mask, T):
-    if mask is not None:
-        if not (isinstance(mask, torch.Tensor) and mask.is_cuda and mask.is_contiguous()
-                and mask.dtype in (torch.uint8, torch.bool) and tuple(mask.shape) == (T,)):
-            raise ValueError(f"token_mask: expected a contiguous uint8 or bool tensor [{T}] on the GPU")
+def _matrix(t, name: str):
+    """(rows, columns) of a two-dimensional tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def moe_balance_loss(logits, topk_ids, expert_counts, prob_mean, group_scale, loss, workspace, token_mask=None,
@@ -376,23 +393,17 @@ def moe_balance_loss(logits, topk_ids, expert_counts, prob_mean, group_scale, lo
     """The balance loss and per-expert counts of ``logits`` [T, E] routed to ``topk_ids`` [T, k];
     ``expert_counts`` (int32) and ``prob_mean`` [G, E] fix the number of groups G, ``group_scale``
     [G] goes to ``moe_route_backward``; ``loss`` [1]; masked tokens (0) are not counted."""
-    _dev(logits, torch.float32, "logits")
-    T, E = logits.shape
-    G = expert_counts.shape[0]
-    _dev(topk_ids, torch.int32, "topk_ids")
-    k = topk_ids.shape[-1]
-    _shaped(topk_ids, torch.int32, "topk_ids", (T, k))
-    _shaped(expert_counts, torch.int32, "expert_counts", (G, E))
-    _shaped(prob_mean, torch.float32, "prob_mean", (G, E))
-    _shaped(group_scale, torch.float32, "group_scale", (G,))
-    _shaped(loss, torch.float32, "loss", (1,))
-    _token_mask(token_mask, T)
-    _dev(workspace, torch.uint8, "workspace")
-    _here(logits=logits, topk_ids=topk_ids, expert_counts=expert_counts, prob_mean=prob_mean,
-          group_scale=group_scale, loss=loss, workspace=workspace, token_mask=token_mask)
-    _check(lib().moe_balance_loss(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k, G, float(coef),
-                                  _ptr(expert_counts), _ptr(prob_mean), _ptr(group_scale), _ptr(loss),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)), "moe_balance_loss")
+    dev = _current(logits, "logits")
+    T, E = _matrix(logits, "logits")
+    k = _matrix(topk_ids, "topk_ids")[1]
+    G = _matrix(expert_counts, "expert_counts")[0]
+    _check(lib().moe_balance_loss(
+        _arg(logits, "logits", _F32, (T, E), dev), _arg(topk_ids, "topk_ids", _I32, (T, k), dev),
+        None if token_mask is None else _arg(token_mask, "token_mask", _MASK, (T,), dev), T, E, k, G, coef,
+        _arg(expert_counts, "expert_counts", _I32, (G, E), dev), _arg(prob_mean, "prob_mean", _F32, (G, E), dev),
+        _arg(group_scale, "group_scale", _F32, (G,), dev), _arg(loss, "loss", _F32, (1,), dev),
+        _arg(workspace, "workspace", _U8, workspace.shape, dev), workspace.numel(), _stream(stream)),
+        "moe_balance_loss")
 
 
 def moe_route_backward(logits, topk_ids, topk_w, d_logits, d_topk_w=None, expert_counts=None, group_scale=None,
@@ -400,47 +411,31 @@ def moe_route_backward(logits, topk_ids, topk_w, d_logits, d_topk_w=None, expert
     """``d_logits`` [T, E] of the gate weights (``d_topk_w`` [T, k], or none) and of the balance loss
     (``expert_counts`` [G, E] and ``group_scale`` [G] from ``moe_balance_loss``, ``d_loss`` [1]; or none
     of the three)."""
-    _dev(d_logits, torch.float32, "d_logits")
-    T, E = d_logits.shape
-    _dev(topk_ids, torch.int32, "topk_ids")
-    k = topk_ids.shape[-1]
-    G = 1
-    _shaped(logits, torch.float32, "logits", (T, E))
-    _shaped(topk_ids, torch.int32, "topk_ids", (T, k))
-    _shaped(topk_w, torch.float32, "topk_w", (T, k))
-    if d_topk_w is not None:
-        _shaped(d_topk_w, torch.float32, "d_topk_w", (T, k))
-    if expert_counts is not None:
-        G = expert_counts.shape[0]
-        _shaped(expert_counts, torch.int32, "expert_counts", (G, E))
-    if group_scale is not None:
-        _shaped(group_scale, torch.float32, "group_scale", (G,))
-    if d_loss is not None:
-        _shaped(d_loss, torch.float32, "d_loss", (1,))
-    _token_mask(token_mask, T)
-    _here(logits=logits, topk_ids=topk_ids, topk_w=topk_w, d_logits=d_logits, d_topk_w=d_topk_w,
-          expert_counts=expert_counts, group_scale=group_scale, d_loss=d_loss, token_mask=token_mask)
-    _check(lib().moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(d_topk_w), _ptr(expert_counts),
-                                    _ptr(group_scale), _ptr(d_loss), _ptr(token_mask), T, E, k, G, _ptr(d_logits),
-                                    _stream(stream)), "moe_route_backward")
+    dev = _current(d_logits, "d_logits")
+    T, E = _matrix(d_logits, "d_logits")
+    k = _matrix(topk_ids, "topk_ids")[1]
+    G = 1 if expert_counts is None else _matrix(expert_counts, "expert_counts")[0]
+    _check(lib().moe_route_backward(
+        _arg(logits, "logits", _F32, (T, E), dev), _arg(topk_ids, "topk_ids", _I32, (T, k), dev),
+        _arg(topk_w, "topk_w", _F32, (T, k), dev),
+        None if d_topk_w is None else _arg(d_topk_w, "d_topk_w", _F32, (T, k), dev),
+        None if expert_counts is None else _arg(expert_counts, "expert_counts", _I32, (G, E), dev),
+        None if group_scale is None else _arg(group_scale, "group_scale", _F32, (G,), dev),
+        None if d_loss is None else _arg(d_loss, "d_loss", _F32, (1,), dev),
+        None if token_mask is None else _arg(token_mask, "token_mask", _MASK, (T,), dev), T, E, k, G,
+        _arg(d_logits, "d_logits", _F32, (T, E), dev), _stream(stream)), "moe_route_backward")
 
 
 def moe_combine_backward(d_out, y_sorted, topk_w, pair_to_sorted, d_y_sorted=None, d_topk_w=None, stream=None):
     """Gradient of ``moe_combine``: ``d_y_sorted`` (fp16, the shape of ``y_sorted``) and ``d_topk_w``
     (fp32 [T, k]), either may be None."""
-    _dev(d_out, torch.float32, "d_out")
-    T, H = d_out.shape
-    _dev(topk_w, torch.float32, "topk_w")
-    k = topk_w.shape[-1]
-    _shaped(topk_w, torch.float32, "topk_w", (T, k))
-    _shaped(pair_to_sorted, torch.int32, "pair_to_sorted", (T * k,))
-    for t, name in ((y_sorted, "y_sorted"), (d_y_sorted, "d_y_sorted")):
-        if t is not None and not (t.is_cuda and t.is_contiguous() and t.dtype in (torch.float16, torch.int16)
-                                  and tuple(t.shape) == (T * k, H)):
-            raise ValueError(f"{name}: expected a contiguous fp16 tensor {(T * k, H)} on the GPU")
-    if d_topk_w is not None:
-        _shaped(d_topk_w, torch.float32, "d_topk_w", (T, k))
-    _here(d_out=d_out, y_sorted=y_sorted, topk_w=topk_w, pair_to_sorted=pair_to_sorted, d_y_sorted=d_y_sorted,
-          d_topk_w=d_topk_w)
-    _check(lib().moe_combine_backward(_ptr(d_out), _ptr(y_sorted), _ptr(topk_w), _ptr(pair_to_sorted), T, k, H,
-                                      _ptr(d_y_sorted), _ptr(d_topk_w), _stream(stream)), "moe_combine_backward")
+    dev = _current(d_out, "d_out")
+    T, H = _matrix(d_out, "d_out")
+    k = _matrix(topk_w, "topk_w")[1]
+    _check(lib().moe_combine_backward(
+        _arg(d_out, "d_out", _F32, (T, H), dev),
+        None if y_sorted is None else _arg(y_sorted, "y_sorted", _F16, (T * k, H), dev),
+        _arg(topk_w, "topk_w", _F32, (T, k), dev), _arg(pair_to_sorted, "pair_to_sorted", _I32, (T * k,), dev), T, k, H,
+        None if d_y_sorted is None else _arg(d_y_sorted, "d_y_sorted", _F16, (T * k, H), dev),
+        None if d_topk_w is None else _arg(d_topk_w, "d_topk_w", _F32, (T, k), dev), _stream(stream)),
+        "moe_combine_backward")

@@ -5,6 +5,11 @@
 // Every pair owns its row of y_sorted, so nothing is accumulated across
 // tokens and there are no atomics.  Bound by HBM: 2 k H bytes of y read and
 // 2 k H of d_y written per token, 4 H of d_out read.
+//
+// One block per token; a thread owns 8 columns of a pass, holds their d_out in
+// registers and takes CW_J rows at a time, all loaded before the first is used.
+// The CW_J products' sums stay in registers over the passes, then go over the
+// lanes and, through LDS, over the waves.
 #include "common.h"
 #include "kernels.h"
 
@@ -13,49 +18,68 @@
 namespace moe {
 namespace {
 
-constexpr int CW_THREADS = 256;
+constexpr int CW_J = 8;
 
-__global__ __launch_bounds__(CW_THREADS)
+template <int THREADS>
+__global__ __launch_bounds__(THREADS)
 void combine_backward_kernel(const float* __restrict__ d_out, const uint16_t* __restrict__ y,
                              const float* __restrict__ w, const int32_t* __restrict__ p2s, int T, int k, int H,
                              uint16_t* __restrict__ d_y, float* __restrict__ d_w) {
-    __shared__ float red[MAX_TOPK][CW_THREADS / WAVE];
+    constexpr int WAVES = THREADS / WAVE;
+    __shared__ float red[WAVES][MAX_TOPK];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (size_t t = blockIdx.x; t < (size_t)T; t += gridDim.x) {
         const float* go = d_out + t * H;
-        for (int j = 0; j < k; ++j) {
-            const size_t row = (size_t)p2s[t * k + j] * H;
-            const float wj = d_y ? w[t * k + j] : 0.0f;
-            float dot = 0.0f;
-            for (int h = tid * 8; h < H; h += CW_THREADS * 8) {
-                const float4 a = *reinterpret_cast<const float4*>(go + h);
-                const float4 b = *reinterpret_cast<const float4*>(go + h + 4);
-                const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int32_t* pt = p2s + t * k;
+        for (int j0 = 0; j0 < k; j0 += CW_J) {
+            float dot[CW_J];
+#pragma unroll
+            for (int j = 0; j < CW_J; ++j) dot[j] = 0.0f;
+            for (int h = tid * 8; h < H; h += THREADS * 8) {
+                const float4 ga = *reinterpret_cast<const float4*>(go + h);
+                const float4 gb = *reinterpret_cast<const float4*>(go + h + 4);
+                u32x4 q[CW_J];
                 if (d_w) {
-                    const f16x8 q = __builtin_bit_cast(f16x8, ldg16_stream(y + row + h));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot = fmaf(v[i], (float)q[i], dot);
+                    for (int j = 0; j < CW_J; ++j)
+                        if (j0 + j < k) q[j] = ldg16_stream(y + (size_t)pt[j0 + j] * H + h);
                 }
-                if (d_y) {
-                    f16x8 o;
+                const float v[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = (_Float16)(wj * v[i]);
-                    stg16(d_y + row + h, __builtin_bit_cast(u32x4, o));
+                for (int j = 0; j < CW_J; ++j) {
+                    if (j0 + j >= k) break;
+                    if (d_y) {
+                        const float wj = w[t * k + j0 + j];
+                        f16x8 o;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = (_Float16)(wj * v[i]);
+                        stg16(d_y + (size_t)pt[j0 + j] * H + h, __builtin_bit_cast(u32x4, o));
+                    }
+                    if (d_w) {
+                        const f16x8 f = __builtin_bit_cast(f16x8, q[j]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[j] = fmaf(v[i], (float)f[i], dot[j]);
+                    }
                 }
             }
             if (d_w) {
 #pragma unroll
-                for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
-                if (lane == 0) red[j][wave] = dot;
+                for (int j = 0; j < CW_J; ++j) {
+                    if (j0 + j >= k) break;
+                    float s = dot[j];
+#pragma unroll
+                    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+                    if (lane == 0) red[wave][j0 + j] = s;
+                }
             }
         }
         if (d_w) {
             __syncthreads();
             if (tid < k) {
-                float v = 0.0f;
+                float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < CW_THREADS / WAVE; ++i) v += red[tid][i];
-                d_w[t * k + tid] = v;
+                for (int i = 0; i < WAVES; ++i) s += red[i][tid];
+                d_w[t * k + tid] = s;
             }
             __syncthreads();
         }
@@ -66,7 +90,10 @@ void combine_backward_kernel(const float* __restrict__ d_out, const uint16_t* __
 
 hipError_t launch_combine_backward(const float* d_out, const uint16_t* y, const float* w, const int32_t* p2s, int T,
                                    int k, int H, uint16_t* d_y, float* d_w, hipStream_t s) {
-    combine_backward_kernel<<<(unsigned)std::min(T, 1 << 20), CW_THREADS, 0, s>>>(d_out, y, w, p2s, T, k, H, d_y, d_w);
+    const unsigned blocks = (unsigned)std::min(T, 1 << 20);
+    if (H <= 512) combine_backward_kernel<64><<<blocks, 64, 0, s>>>(d_out, y, w, p2s, T, k, H, d_y, d_w);
+    else if (H <= 2048) combine_backward_kernel<256><<<blocks, 256, 0, s>>>(d_out, y, w, p2s, T, k, H, d_y, d_w);
+    else combine_backward_kernel<512><<<blocks, 512, 0, s>>>(d_out, y, w, p2s, T, k, H, d_y, d_w);
     return hipGetLastError();
 }
 
