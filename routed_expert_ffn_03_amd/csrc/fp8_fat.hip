@@ -5,25 +5,42 @@
 //
 //   acc[n, m] += (sum_{k in block b} w[n, k] x[m, k]) * (sx[m, b] * sw[n/128, b])
 //
-// One 512-thread block per CU, persistent.  A stage is one 128-column block,
-// so a row of a stage is one whole 128-byte line: the per-CU load path moves
-// about a line per clock however much of it is used.  Operands go through LDS
-// by direct-to-LDS loads (8 rows x 128 B per instruction): three slots of
-// weight rows (32 KB), which mostly come from HBM and are loaded two stages
-// ahead, and two of activation rows (28 KB) with their 224 row scales, loaded
-// one stage ahead (mostly L2).  224 rows rather than 256 leave room for the
-// scales in the 160 KB of LDS.  16-byte piece c of row r lies at position
-// c ^ (r & 7) ^ ((r >> 3) & 1) of its line, so that 8 lanes reading the same
-// piece of 8 consecutive rows hit all banks once.
+// Products.  A 128-column block is one 16x16x128 MFMA per 16 x 16 tile, into a
+// fresh partial sum; its four fmas with the block's scale (one value per lane,
+// because the activation rows are the MFMA's columns) follow four products
+// later, so they run beside the next tile's.  Register-only probes on random
+// codes: 32x32x64 pairs with their fmas 3.0 PF, 16x16x128 with the fmas three
+// or four products behind 3.5 PF (4.0 PF without fmas, 5.0 PF on zeros: power
+// sets the clock).
 //
-// Wave (G, q) owns 64 weight rows (phase 1: gate rows 32 q .. and up rows
-// 32 q ..; phase 2: rows 64 q ..) against row tiles G, G + 2, G + 4, G + 6:
-// the two waves of a SIMD share the work of any M-tile to within one row
-// tile, and while one multiplies its partial sums into the accumulators the
-// other's MFMAs run.  The products of one 32 x 32 tile over a stage are two
-// 32x32x64 MFMAs into a fresh partial sum, then 16 fmas with the block's
-// scale, one value per lane because the activation rows are the MFMA's
-// columns.
+// Operands.  One 512-thread block per CU, persistent.  A stage is one
+// 128-column block, so a row of a stage is one whole 128-byte line.  Weight
+// rows (32 KB a stage) go through three LDS slots and activation rows (28 KB)
+// with their scales through two, by direct-to-LDS loads of 8 rows x 128 B,
+// issued one at a time between the products (all at the stage's start: 5%
+// slower).  16-byte piece c of row r lies at position c ^ (r & 7) ^ ((r >> 3)
+// & 1) of its line, so that 8 lanes reading the same piece of 8 consecutive
+// rows hit all banks once.  224 rows rather than 256 leave room for the scales.
+//
+// Waves.  Wave (G, q) owns 64 weight rows (phase 1: gate rows 32 q .. and up
+// rows 32 q ..; phase 2: rows 64 q ..) against the 16-row tiles G, G + 2, ...:
+// the two waves of a SIMD share the work of any M-tile to within one tile.
+// The 64 weight rows' fragments stay in registers for a stage, row fragments
+// are read two tiles ahead, and one barrier per stage, before its last tile but
+// one, says that the next stage's operands have landed and this stage's rows
+// have been read.  The next item's first loads go out before the epilogue.
+//
+// What bounds it (16,384 tokens, 384 experts, 4096 x 2048, top-8, one
+// MI355X): gate/up 2.55 ms and down 1.40 ms, 1.67 PF over both.  The MFMAs are
+// busy 45% of the cycles at a clock that the power limit holds at 1.83 GHz
+// (2.2 GHz with the loads taken out); taking cycles out of a stage or an
+// epilogue mostly lowers that clock further.  Loads cost the rest: without
+// them gate/up takes 1.7 ms.  Half of the weight reads miss L2, since the two
+// blocks that share a weight tile drift apart (11 GB of 6.4 GB).
+// Measured and not kept: the two waves of a SIMD in turns with two barriers a
+// stage (3.05 / 1.54 ms), 32x32x64 products (2.70 / 1.45), the next stage's
+// weights in a second set of registers (3.0 / 1.6), items starting at
+// different columns (no change), 192 rows (1.5% slower).
 #include "common.h"
 #include "ffn_shared.h"
 #include "fp8.h"
@@ -216,8 +233,9 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 for (int i = 0; i < RA; ++i) acc[i][c] = f32x4{};
             }
             float f0 = 0.0f, f1 = 0.0f;                            // scales of the partial sums in p
-            u32x4 w[4][2], x[NB][2], sx0, sx1;                    // weights by column tile, rows in a ring of three tiles
-            u32x2 swv;                                             // (sx0, sx1: row scales of tiles 0-3, 4-6) block scales
+            u32x4 w[4][2], x[NB][2];                               // weights by column tile, rows in a ring of tiles
+            u32x4 sx0, sx1;                                        // row scales of tiles 0-3 and 4-6
+            u32x2 swv;                                             // block scales
             auto read_w = [&](auto c_c, int kt) {
                 constexpr int C = decltype(c_c)::value;
                 const uint32_t wb = wslot(kt) * FF_W + wfo;
@@ -246,19 +264,18 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
                 tie_after_wait(swv);
             };
 
-            // One stage.  LDS returns in
-            // order, so a wait for all but the N newest reads is a wait for
-            // the older ones.  Reads run two tiles ahead: at tile t those of
-            // tile t + 2; before the last tile but one every wave has all
-            // rows of this stage (barrier: the rows, and the weights read in
-            // the stage before, make room for loads of later stages), and
-            // from there on the next stage's first two tiles, its scales and,
-            // behind the products that used the old ones, its weights (past the
-            // last stage: whatever lies there, unused).
+            // One stage.  LDS returns in order, so a wait for all but the N
+            // newest reads is a wait for the older ones.  Reads run two tiles
+            // ahead: at tile t those of tile t + 2.  Before the last tile but
+            // one every wave has all rows of this stage and the weights of
+            // this stage, read in the stage before (barrier: their slots are
+            // free); from there on come the next stage's first two tiles and,
+            // behind the products that used the old ones, its weights and
+            // scales (past the last stage: whatever lies there, unused).
             auto stage = [&](int kt) {
                 const bool more = kt + 1 < KB;
                 auto boundary = [&]() {
-                    // the rows of stage kt + 1 and the weights of stage kt + 1: all but the newest weights
+                    // this wave's loads of stage kt + 1: all but the weights of stage kt + 2
                     if (kt + 2 < KB) vm_wait<4>(); else vm_wait<0>();
                     barrier();
                 };
