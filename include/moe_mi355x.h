@@ -236,13 +236,15 @@ moe_status moe_grouped_ffn(const uint16_t* x, int wfmt,
  * (fp32) in its epilogue:
  *     g[n] = sum_b sx[t, b] s_gate[n/128, b] sum_{h in b} xq[t, h] w_gate[n, h]
  * and likewise u, and y from the codes of a and w_down.  Each 128-column
- * product is taken on the e4m3 MFMA and takes both scales before it is added
- * in fp32.  The MFMA adds eight consecutive products at a time, each cut 13
- * bits below the largest of them, and these sums in fp32: about 1.5e-5 of a
- * 128-column sum of normally distributed codes.  Where that moves a across a
- * rounding border its code is the neighbour: y is about 1e-3 of its norm from
- * exact sums of the same codes (rounding to e4m3 itself costs about 3e-2).  NaN or infinite values of x or a become the NaN code and make their
- * rows of y NaN.  x, the weights and y_sorted must be 16-byte aligned, the
+ * product takes both scales before it is added in fp32.  Short route lists
+ * multiply the codes exactly and add in fp32.  Lists in M-tiles use the e4m3
+ * MFMA, which adds eight consecutive products at a time, each cut 13 bits
+ * below the largest of them: about 1.5e-5 of a 128-column sum of normally
+ * distributed codes.  Where that moves a across a rounding border its code is
+ * the neighbour, and y is about 1e-3 of its norm from exact sums of the same
+ * codes (short lists: 2e-4; rounding to e4m3 itself costs about 3e-2).
+ * NaN or infinite values of x or a become the NaN code and make their rows of
+ * y NaN. x, the weights and y_sorted must be 16-byte aligned, the
  * scales 4-byte, else MOE_ERR_INVALID_ARG; shapes as for the other formats.
  */
 
@@ -401,7 +403,7 @@ size_t moe_balance_workspace_size(int T, int E, int groups);
  * token_mask   uint8 [T] or NULL: tokens with 0 are not counted, and their
  *              logits and ids are not read (padding may hold anything).
  * Logits of counted tokens may be -inf (probability 0; all -inf: p = 0); NaN
- * or +inf make the outputs of their group and the loss NaN.  Ids outside
+ * or +inf make prob_mean of their group and the loss NaN.  Ids outside
  * [0, E) are not counted.  Sums are fp32 in a fixed order, no float atomics:
  * bit-identical across runs.  Two launches.
  * Errors: NULL pointers (token_mask aside), T, E, k as moe_route_topk, groups

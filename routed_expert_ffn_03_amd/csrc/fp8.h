@@ -6,13 +6,15 @@
 // activation row and per 128 x 128 block of a weight matrix; a value is
 // code * scale.  A product over 128 columns takes both scales at once:
 //   y[i, n] = sum_b sx[i, b] sw[n / 128, b] sum_{k in b} xq[i, k] wq[n, k],
-// the outer sum in fp32.  The inner one is the e4m3 MFMA's, which holds fewer
-// bits: it adds the products of eight consecutive k with each cut 13 bits below
-// the largest of them (measured: next to 2^16 a term of 2^3 is kept and 2^2
-// lost, in every shape of the instruction), and these octets in fp32.  That is
-// 1.5e-5 rms of a 128-column sum of normally distributed codes, against 3e-2
-// that rounding x and a to e4m3 costs; products of the codes as bf16 would
-// keep the sums in fp32 at half the MFMA rate.
+// the outer sum in fp32.  The inner one: where a kernel streams weights from
+// HBM the codes are multiplied as fp16, which holds every code exactly, in the
+// fp16 MFMA's fp32 sums.  The M-tiles take the e4m3 MFMA, at twice the rate and
+// with fewer bits: it adds the products of eight consecutive k with each cut 13
+// bits below the largest of them (measured: next to 2^16 a term of 2^3 is kept
+// and 2^2 lost, in every shape of the instruction), and these octets in fp32.
+// That is 1.5e-5 rms of a 128-column sum of normally distributed codes; y ends
+// 1e-3 of its norm from exact sums, against 3e-2 that rounding x and a to e4m3
+// costs.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -28,19 +30,19 @@ constexpr int FP8_BM = 224;              // rows per MFMA M-tile: leaves LDS for
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
-// 32 x 32 x 64 e4m3 products without hardware scales: lane L holds row (A)
-// or column (B) L % 32 and 32 bytes of k; any assignment of k to the lanes'
-// bytes will do that A and B share.  Result element i of lane L is row
-// 8 (i / 4) + 4 (L / 32) + i % 4, column L % 32.
-__device__ __forceinline__ f32x16 mfma_fp8(i32x8 a, i32x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-}
-
 // 16 x 16 x 128 e4m3 products: lane L holds row (A) or column (B) L % 16 and
 // 32 bytes of k.  Result element i of lane L is row 4 (L / 16) + i, column
 // L % 16.
 __device__ __forceinline__ f32x4 mfma16_fp8(i32x8 a, i32x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// Eight e4m3 codes as fp16, which holds every one of them exactly.
+__device__ __forceinline__ u32x4 fp8_to_f16(uint32_t lo, uint32_t hi) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true))};
 }
 
 __device__ __forceinline__ i32x8 pack8(u32x4 lo, u32x4 hi) {

@@ -3,10 +3,10 @@
 //   a      = silu(xq Wg^T) * (xq Wu^T)
 //   aq, sa = e4m3 rows of a
 //   y      = aq Wd^T, stored fp16
-// with every 128-column partial product taken in fp32 on the MFMA and
-// multiplied by its two scales before it is added (fp8.h).  Busy experts run
-// as MFMA tiles (fp8_fat.hip); here are the phases and the streaming kernel of
-// the short route lists, which includes all of a decode step.
+// with every 128-column partial product multiplied by its two scales before it
+// is added in fp32 (fp8.h).  Busy experts run as MFMA tiles (fp8_fat.hip); here
+// are the phases and the streaming kernel of the short route lists, which
+// includes all of a decode step.
 //
 // The weights are the MFMA's A operand and the activation rows its B operand,
 // so that a lane's result registers all belong to one activation row: the row
@@ -19,11 +19,17 @@
 // index, so no partial sums cross waves; phase 1 exchanges the row maxima of
 // its 128 columns, which are one scale group of a, and stores codes.  Every
 // weight is used once, so it is bound by HBM reads: a wave streams its 64 rows
-// through its own two-slot LDS ring, one 128-column block (8 KB) in flight
-// while the one before is multiplied, by direct-to-LDS loads of 8 rows x 128
-// bytes with the non-temporal hint (whole lines).  The first block of the next
-// item is in flight over the epilogue.  Activation rows come straight into
-// registers; they are a few KB that stay in L2.
+// through its own two-slot LDS ring by direct-to-LDS loads of 8 rows x 128
+// bytes with the non-temporal hint (whole lines).  A block of 128 columns
+// (8 KB) goes to registers at once, so that two are in flight while it is
+// multiplied, across items too.  Activation rows come straight into registers,
+// one block ahead; they are a few KB that stay in L2.  The products are fp16
+// ones of the converted codes, exact and summed in fp32: half the e4m3 rate
+// and two conversions for each pair of codes, which hide under the loads
+// (4 tokens on 25 experts of 4096 x 2048, one MI355X: gate/up 70 us and down
+// 38 us, 6.0 and 5.5 TB/s of weights, 1 us each more than with e4m3 products;
+// 1,024 tokens, 327 short lists: 0.83 and 0.47 ms, 6.4 TB/s, the same either
+// way), and y is five times as close to exact sums.
 #include "common.h"
 #include "ffn_shared.h"
 #include "fp8.h"
@@ -62,11 +68,14 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
     typedef const __attribute__((address_space(4))) float* cfloat_t;
     struct Item {
         int e, row0, rows, nt;
+        uint32_t bytes;                              // of its weights that may be loaded
     };
-    auto load_item = [&](int it) {                   // items past the end are clamped: valid addresses, never used
+    // items past the end: the last one, with no weights in range (their loads
+    // count and go nowhere)
+    auto load_item = [&](int it) {
         const int ic = min(it, n_items - 1), nt = ic / n_mt;
         const ctile_t tp = (ctile_t)a.thin + __builtin_amdgcn_readfirstlane(ic - nt * n_mt);
-        return Item{tp->e, tp->row0, tp->rows, nt};
+        return Item{tp->e, tp->row0, tp->rows, nt, it < n_items ? (uint32_t)wbytes : 0u};
     };
     // load instruction i moves rows 8 i .. 8 i + 7: lane L row L / 8, position
     // L % 8, which holds piece (L % 8) ^ (row & 7) ^ ((row >> 3) & 1)
@@ -76,8 +85,8 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
     for (int i = 0; i < 2; ++i) po[i] = (uint32_t)(((lane & 7) ^ lr ^ i) * 16);
     auto issue_w = [&](const Item& q, int ch, int sl) {
         const size_t eoff = (size_t)q.e * wbytes;
-        const __amdgpu_buffer_rsrc_t w0 = make_rsrc((PHASE == 1 ? a.wg : a.wd) + eoff, (uint32_t)wbytes);
-        const __amdgpu_buffer_rsrc_t w1 = PHASE == 1 ? make_rsrc(a.wu + eoff, (uint32_t)wbytes) : w0;
+        const __amdgpu_buffer_rsrc_t w0 = make_rsrc((PHASE == 1 ? a.wg : a.wd) + eoff, q.bytes);
+        const __amdgpu_buffer_rsrc_t w1 = PHASE == 1 ? make_rsrc(a.wu + eoff, q.bytes) : w0;
         const uint32_t r0 = (uint32_t)(PHASE == 1 ? q.nt * 128 + 32 * wave : q.nt * 256 + 64 * wave) + lr;
         char* st = ring + (wave * FS_SLOTS + sl) * FS_CHUNK;
 #pragma unroll
@@ -94,38 +103,58 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) fo[h][j] = base + (uint32_t)(((4 * h + 2 * g + j) ^ (m & 7) ^ ((m >> 3) & 1)) * 16);
 
-    Item cur = load_item(item);
-    issue_w(cur, 0, 0);
+    // Loads run two blocks ahead of the products, across items: block
+    // (issue, ich) goes out next.
+    int issue = item, ich = 0;
+    Item qi = load_item(item);
+    auto issue_next = [&](int sl) {
+        issue_w(qi, ich, sl);
+        if (++ich == KB) {
+            ich = 0;
+            issue += gridDim.x;
+            qi = load_item(issue);
+        }
+    };
+    // Activation rows run one block ahead, their route-list entries two.
+    // (Rows past a tile repeat its last one; they are never stored.)
+    auto entry = [&](const Item& q) {
+        const int row = q.row0 + min(m, q.rows - 1);
+        return PHASE == 1 ? a.sorted_pair[row] : row;
+    };
+    Item cur = qi;
+    int en = entry(qi), src = PHASE == 1 ? en / a.k : en, xch = 0;
+    bool fresh = false;                              // src is of the item before, en of this one
+    u32x4 xf[2][2];
+    float sx;
+    auto issue_x = [&](int ch) {
+        const uint8_t* x = (PHASE == 1 ? a.xq : a.act) + (size_t)src * K + ch * FP8_BLOCK + 32 * g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) xf[h][j] = ldg16(x + 64 * h + 16 * j);
+        sx = PHASE == 1 ? a.xs[(size_t)src * KB + ch] : a.as[(size_t)ch * P + src];
+    };
+    auto next_x = [&]() {                            // rows of block xch; look up those of the block after it
+        issue_x(xch);
+        xch = ich;
+        fresh = ich == 0;
+        if (fresh) en = entry(qi);
+    };
+    issue_next(0);
+    next_x();
+    __builtin_amdgcn_sched_barrier(0);
+    issue_next(1);
     for (int sl = 0, par = 0;; par ^= 1) {
         const Item nxt = load_item(item + gridDim.x);
-        // rows past the tile repeat its last one; they are never stored
         const int row = cur.row0 + min(m, cur.rows - 1);
-        const size_t src = PHASE == 1 ? (size_t)(a.sorted_pair[row] / a.k) : (size_t)row;
-        const uint8_t* x = (PHASE == 1 ? a.xq : a.act) + src * K + 32 * g;
-        const float* xs = PHASE == 1 ? a.xs + src * KB : a.as + src;
-        const size_t xstep = PHASE == 1 ? 1 : P;
         const size_t soff = (size_t)cur.e * (N / FP8_BLOCK) * KB;
         const cfloat_t s0 = (cfloat_t)(PHASE == 1 ? a.sg + soff + (size_t)cur.nt * KB
                                                   : a.sd + soff + (size_t)(2 * cur.nt + (wave >> 1)) * KB);
         const cfloat_t s1 = PHASE == 1 ? (cfloat_t)(a.su + soff + (size_t)cur.nt * KB) : s0;
-        u32x4 xf[2][2];
-        float sx;
-        auto issue_x = [&](int ch) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) xf[h][j] = ldg16(x + ch * FP8_BLOCK + 64 * h + 16 * j);
-            sx = xs[ch * xstep];
-        };
         f32x16 acc[2] = {f32x16{}, f32x16{}};
-        issue_x(0);
         for (int ch = 0; ch < KB; ++ch) {
-            // the block after this one (of the next item at the end; past the
-            // last item a repeat that nobody reads), then everything older
-            const bool end = ch + 1 == KB;
-            issue_w(end ? nxt : cur, end ? 0 : ch + 1, sl ^ 1);
             const float f0 = s0[ch], f1 = s1[ch];
-            vm_wait<8>();
+            vm_wait<8>();                            // all but the block after this one
             const uint32_t so = (uint32_t)sl * FS_CHUNK;
             u32x4 w[2][2][2];
             static_for<2>([&](auto h_c) {
@@ -135,6 +164,15 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
                     w[1][Hh][J] = ds_read16<32 * 128>(fo[Hh][J] + so);
                 });
             });
+            u32x4 xh[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const u32x4 v = xf[i >> 2][(i >> 1) & 1];
+                xh[i] = fp8_to_f16(v[2 * (i & 1)], v[2 * (i & 1) + 1]);
+            }
+            const float g0 = sx * f0, g1 = PHASE == 1 ? sx * f1 : g0;
+            if (fresh) src = PHASE == 1 ? en / a.k : en;
+            next_x();
             lds_wait_all();
             static_for<2>([&](auto h_c) {
                 static_for<2>([&](auto j_c) {
@@ -143,13 +181,16 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
                     tie_after_wait(w[1][Hh][J]);
                 });
             });
-            const i32x8 x0 = pack8(xf[0][0], xf[0][1]), x1 = pack8(xf[1][0], xf[1][1]);
-            f32x16 p0 = mfma_fp8(pack8(w[0][0][0], w[0][0][1]), x0, f32x16{});
-            f32x16 p1 = mfma_fp8(pack8(w[1][0][0], w[1][0][1]), x0, f32x16{});
-            p0 = mfma_fp8(pack8(w[0][1][0], w[0][1][1]), x1, p0);
-            p1 = mfma_fp8(pack8(w[1][1][0], w[1][1][1]), x1, p1);
-            const float g0 = sx * f0, g1 = PHASE == 1 ? sx * f1 : g0;
-            issue_x(min(ch + 1, KB - 1));
+            __builtin_amdgcn_sched_barrier(0);
+            issue_next(sl);                          // the slot is in registers
+            __builtin_amdgcn_sched_barrier(0);
+            f32x16 p0 = f32x16{}, p1 = f32x16{};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const u32x4 u = w[0][i >> 2][(i >> 1) & 1], v = w[1][i >> 2][(i >> 1) & 1];
+                p0 = mfma_f16(fp8_to_f16(u[2 * (i & 1)], u[2 * (i & 1) + 1]), xh[i], p0);
+                p1 = mfma_f16(fp8_to_f16(v[2 * (i & 1)], v[2 * (i & 1) + 1]), xh[i], p1);
+            }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 acc[0][r] = fmaf(p0[r], g0, acc[0][r]);
@@ -193,7 +234,7 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
         if (item >= n_items) break;
         cur = nxt;
     }
-    vm_wait<0>();                                    // the unused last block has landed
+    vm_wait<0>();                                    // the unused last blocks have landed
 }
 
 }  // namespace
