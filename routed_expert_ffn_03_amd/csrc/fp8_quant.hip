@@ -3,7 +3,8 @@
 //
 // code = e4m3(v / s), s the least power of two >= 2^-126 with max|v| <= 448 s
 // over the block's finite values (fp8.h).  Bound by HBM: 2 bytes read, 1
-// written per value.
+// written per value.  One MI355X: 16,384 rows of 4096 37 us (5.4 TB/s), 32
+// weights of 2048 x 4096 142 us (5.7 TB/s); 4 rows 2.7 us, which is a launch.
 //
 // Rows: 16 lanes per group, 8 values each (one 16-byte load, one 8-byte
 // store), the maximum by four lane exchanges.  Weights: one 256-thread block
