@@ -1,7 +1,7 @@
 """Static checks of the gfx950 assembly of the 8-bit expert kernels (CPU only).
 
 1. No instruction touches the destination of an LDS read before a wait has
-   retired it, the checker of tests/asm_check.py with one refinement: where
+   retired it, by the analysis of tests/asm_check.py with one refinement: where
    two paths meet with the same newest reads in flight (the MFMA-tile kernel
    carries reads over its loop's back edge), their order is kept, so that a
    wait for all but the N newest of them counts.
