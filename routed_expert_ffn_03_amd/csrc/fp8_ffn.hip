@@ -14,9 +14,11 @@
 // four consecutive result registers are four consecutive output columns.
 //
 // Streaming kernel.  Work item: (a tile of up to 32 rows, 128 columns of a or
-// 256 of y), one 256-thread block; wave w owns 32 gate and the matching 32 up
-// rows (phase 1) or 64 rows of W_down (phase 2) over the whole reduction
-// index, so no partial sums cross waves; phase 1 exchanges the row maxima of
+// 64 of y).  A wave owns 32 gate and the matching 32 up rows (phase 1, four
+// waves a block) or 64 rows of W_down (phase 2, one wave a block: with four,
+// the 400 items of 4 tokens left a fifth of the CUs' room empty, 40.4 us
+// against 39.2; 1 token 21.3 against 18.0) over the whole reduction index, so
+// no partial sums cross waves; phase 1 exchanges the row maxima of
 // its 128 columns, which are one scale group of a, and stores codes.  Every
 // weight is used once, so it is bound by HBM reads: a wave streams its 64 rows
 // through its own two-slot LDS ring by direct-to-LDS loads of 8 rows x 128
@@ -27,7 +29,7 @@
 // ones of the converted codes, exact and summed in fp32: half the e4m3 rate
 // and two conversions for each pair of codes, which hide under the loads
 // (4 tokens on 25 experts of 4096 x 2048, one MI355X: gate/up 70 us and down
-// 38 us, 6.0 and 5.5 TB/s of weights, 1 us each more than with e4m3 products;
+// 37 us, 6.0 and 5.7 TB/s of weights, 1 us each more than with e4m3 products;
 // 1,024 tokens, 327 short lists: 0.83 and 0.47 ms, 6.4 TB/s, the same either
 // way), and y is five times as close to exact sums.
 #include "common.h"
@@ -39,22 +41,27 @@
 namespace moe {
 namespace {
 
-constexpr int FS_THREADS = 256;
 constexpr uint32_t FS_CHUNK = 64 * 128;              // a wave's 64 weight rows of one block
 constexpr int FS_SLOTS = 2;
-constexpr uint32_t FS_RING = 4 * FS_SLOTS * FS_CHUNK;
+constexpr int FS_CU_WAVES = 8;                       // that fit a CU's LDS
+
+// waves per block
+template <int PHASE>
+constexpr int fs_waves = PHASE == 1 ? 4 : 1;
 
 template <int PHASE>
-__global__ __launch_bounds__(FS_THREADS, 2)
+__global__ __launch_bounds__(fs_waves<PHASE> * 64, 2)
 void ffn_fp8_stream_kernel(Fp8Args a) {
-    __shared__ __attribute__((aligned(1024))) char ring[FS_RING];
-    __shared__ float top[2][4][32];                  // phase 1: row maxima by wave, alternating between items
+    constexpr int NW = fs_waves<PHASE>;
+    constexpr int BN = PHASE == 1 ? 128 : 64 * NW;   // columns of an item
+    __shared__ __attribute__((aligned(1024))) char ring[NW * FS_SLOTS * FS_CHUNK];
+    __shared__ float top[2][NW][32];                  // phase 1: row maxima by wave, alternating between items
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = NW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
     const int m = lane & 31, g = lane >> 5;
     const int K = PHASE == 1 ? a.H : a.I, N = PHASE == 1 ? a.I : a.H;
     const int KB = K / FP8_BLOCK;
-    const int NT = PHASE == 1 ? N / 128 : N / 256;
+    const int NT = N / BN;
     const int n_mt = a.hdr->n_thin;
     const int n_items = n_mt * NT;
     const size_t P = (size_t)a.T * a.k;
@@ -87,7 +94,7 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
         const size_t eoff = (size_t)q.e * wbytes;
         const __amdgpu_buffer_rsrc_t w0 = make_rsrc((PHASE == 1 ? a.wg : a.wd) + eoff, q.bytes);
         const __amdgpu_buffer_rsrc_t w1 = PHASE == 1 ? make_rsrc(a.wu + eoff, q.bytes) : w0;
-        const uint32_t r0 = (uint32_t)(PHASE == 1 ? q.nt * 128 + 32 * wave : q.nt * 256 + 64 * wave) + lr;
+        const uint32_t r0 = (uint32_t)(q.nt * BN + (PHASE == 1 ? 32 : 64) * wave) + lr;
         char* st = ring + (wave * FS_SLOTS + sl) * FS_CHUNK;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -149,7 +156,7 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
         const int row = cur.row0 + min(m, cur.rows - 1);
         const size_t soff = (size_t)cur.e * (N / FP8_BLOCK) * KB;
         const cfloat_t s0 = (cfloat_t)(PHASE == 1 ? a.sg + soff + (size_t)cur.nt * KB
-                                                  : a.sd + soff + (size_t)(2 * cur.nt + (wave >> 1)) * KB);
+                                                  : a.sd + soff + (size_t)((cur.nt * BN + 64 * wave) / FP8_BLOCK) * KB);
         const cfloat_t s1 = PHASE == 1 ? (cfloat_t)(a.su + soff + (size_t)cur.nt * KB) : s0;
         f32x16 acc[2] = {f32x16{}, f32x16{}};
         for (int ch = 0; ch < KB; ++ch) {
@@ -219,7 +226,7 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
                 if (wave == 0 && g == 0) a.as[(size_t)cur.nt * P + row] = s;
             }
         } else if (m < cur.rows) {
-            uint16_t* dst = a.y + (size_t)row * a.H + cur.nt * 256 + 64 * wave + 4 * g;
+            uint16_t* dst = a.y + (size_t)row * a.H + cur.nt * BN + 64 * wave + 4 * g;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -248,8 +255,9 @@ hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipS
         const hipError_t err = launch_fp8_fat_phase(a, phase, cus, s);
         if (err != hipSuccess) return err;
     }
-    if (phase == 1) ffn_fp8_stream_kernel<1><<<2 * cus, FS_THREADS, 0, s>>>(a);
-    else ffn_fp8_stream_kernel<2><<<2 * cus, FS_THREADS, 0, s>>>(a);
+    const int waves = FS_CU_WAVES * cus;
+    if (phase == 1) ffn_fp8_stream_kernel<1><<<waves / fs_waves<1>, fs_waves<1> * 64, 0, s>>>(a);
+    else ffn_fp8_stream_kernel<2><<<waves / fs_waves<2>, fs_waves<2> * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
