@@ -29,7 +29,7 @@
 // ones of the converted codes, exact and summed in fp32: half the e4m3 rate
 // and two conversions for each pair of codes, which hide under the loads
 // (4 tokens on 25 experts of 4096 x 2048, one MI355X: gate/up 70 us and down
-// 37 us, 6.0 and 5.7 TB/s of weights, 1 us each more than with e4m3 products;
+// 37 us, 6.0 and 5.7 TB/s of weights, at most 1 us more than with e4m3 products;
 // 1,024 tokens, 327 short lists: 0.83 and 0.47 ms, 6.4 TB/s, the same either
 // way), and y is five times as close to exact sums.
 #include "common.h"
