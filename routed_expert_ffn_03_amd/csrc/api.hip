@@ -204,6 +204,28 @@ moe_status moe_ffn_down(int wfmt, const void* w_down, const void* s_down, int T,
     return hip_status(moe::launch_ffn_phase(a, 2, reinterpret_cast<hipStream_t>(stream)));
 }
 
+static void set_tensors(moe::FfnLaunch& a, const uint16_t* x, const void* w_gate, const void* w_up,
+                        const void* w_down, const void* s_gate, const void* s_up, const void* s_down,
+                        const int32_t* expert_offsets, const int32_t* sorted_pair, int fat_threshold,
+                        uint16_t* y_sorted) {
+    a.x = x;
+    a.wg = w_gate; a.wu = w_up; a.wd = w_down;
+    a.sg = s_gate; a.su = s_up; a.sd = s_down;
+    a.offsets = expert_offsets;
+    a.sorted_pair = sorted_pair;
+    a.fat_threshold = fat_threshold;
+    a.y = y_sorted;
+}
+
+// plan, gate/up, down
+static moe_status run_ffn(moe::FfnLaunch& a, hipStream_t s) {
+    a.plan_x = a.wfmt == MOE_WFMT_FP8_B128;
+    hipError_t err = moe::launch_ffn_plan(a, s);
+    if (err == hipSuccess) err = moe::launch_ffn_phase(a, 1, s);
+    if (err == hipSuccess) err = moe::launch_ffn_phase(a, 2, s);
+    return hip_status(err);
+}
+
 moe_status moe_grouped_ffn(const uint16_t* x, int wfmt, const void* w_gate, const void* w_up, const void* w_down,
                            const void* s_gate, const void* s_up, const void* s_down,
                            const int32_t* expert_offsets, const int32_t* sorted_pair, int T, int E, int k, int H,
@@ -221,13 +243,8 @@ moe_status moe_grouped_ffn(const uint16_t* x, int wfmt, const void* w_gate, cons
     moe::FfnLaunch a;
     moe_status st = ffn_prepare(a, wfmt, T, E, k, H, I, workspace, workspace_bytes);
     if (st != MOE_OK) return st;
-    st = moe_ffn_plan(expert_offsets, T, E, k, H, I, wfmt, fat_threshold, workspace, workspace_bytes, stream);
-    if (st != MOE_OK) return st;
-    st = moe_ffn_gate_up(x, wfmt, w_gate, w_up, s_gate, s_up, sorted_pair, T, E, k, H, I, fat_threshold, workspace,
-                         workspace_bytes, stream);
-    if (st != MOE_OK) return st;
-    return moe_ffn_down(wfmt, w_down, s_down, T, E, k, H, I, fat_threshold, y_sorted, workspace, workspace_bytes,
-                        stream);
+    set_tensors(a, x, w_gate, w_up, w_down, s_gate, s_up, s_down, expert_offsets, sorted_pair, fat_threshold, y_sorted);
+    return run_ffn(a, reinterpret_cast<hipStream_t>(stream));
 }
 
 moe_status moe_route_permute_plan(const float* logits, int T, int E, int k, int H, int I, int wfmt,
@@ -279,23 +296,13 @@ moe_status moe_grouped_ffn_noalloc(const uint16_t* x, int wfmt, const void* w_ga
     hipError_t err = scratch_address(&ws);
     if (err != hipSuccess) return MOE_ERR_HIP;
     moe::FfnLaunch a{};
-    a.x = x;
     a.wfmt = wfmt;
-    a.wg = w_gate; a.wu = w_up; a.wd = w_down;
-    a.sg = s_gate; a.su = s_up; a.sd = s_down;
-    a.offsets = expert_offsets;
-    a.sorted_pair = sorted_pair;
     a.T = T; a.E = E; a.k = k; a.H = H; a.I = I;
-    a.fat_threshold = fat_threshold;
-    a.y = y_sorted;
     a.ws = ws;
-    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    set_tensors(a, x, w_gate, w_up, w_down, s_gate, s_up, s_down, expert_offsets, sorted_pair, fat_threshold, y_sorted);
     // the plan rewrites the list header, totals and the tail counters of
     // the shared array before the two phases read them
-    err = moe::launch_ffn_plan(a, s);
-    if (err == hipSuccess) err = moe::launch_ffn_phase(a, 1, s);
-    if (err == hipSuccess) err = moe::launch_ffn_phase(a, 2, s);
-    return hip_status(err);
+    return run_ffn(a, reinterpret_cast<hipStream_t>(stream));
 }
 
 moe_status moe_pack_bf16_pairs(const uint16_t* src, uint16_t* dst, int64_t mats, int rows, int cols, int to_fp16,

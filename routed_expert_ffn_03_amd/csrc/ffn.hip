@@ -59,9 +59,9 @@ namespace {
 
 // ------------------------------------------------------------ tile builder
 
-__global__ __launch_bounds__(1024)
-void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, int bm, FfnHeader* __restrict__ hdr,
-                        MTile* __restrict__ fat, MTile* __restrict__ thin, int32_t* __restrict__ counts) {
+__device__ __forceinline__ void build_tiles(const int32_t* __restrict__ offsets, int E, int thr, int bm,
+                                            FfnHeader* __restrict__ hdr, MTile* __restrict__ fat,
+                                            MTile* __restrict__ thin, int32_t* __restrict__ counts) {
     __shared__ int scratch[16];
     const int e = threadIdx.x;
     int n = 0, nf = 0, nt = 0, r0 = 0;
@@ -81,6 +81,26 @@ void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, int
         hdr->tail_next[0] = hdr->tail_next[1] = 0;
         hdr->tail_done[0] = hdr->tail_done[1] = 0;
     }
+}
+
+__global__ __launch_bounds__(1024)
+void build_tiles_kernel(const int32_t* __restrict__ offsets, int E, int thr, int bm, FfnHeader* __restrict__ hdr,
+                        MTile* __restrict__ fat, MTile* __restrict__ thin, int32_t* __restrict__ counts) {
+    build_tiles(offsets, E, thr, bm, hdr, fat, thin, counts);
+}
+
+// The tile builder and, in the blocks after its one, the e4m3 codes of x: two
+// launches in one for whole calls.
+__global__ __launch_bounds__(1024)
+void build_tiles_quant_kernel(const int32_t* __restrict__ offsets, int E, int thr, int bm, FfnHeader* __restrict__ hdr,
+                              MTile* __restrict__ fat, MTile* __restrict__ thin, const uint16_t* __restrict__ x,
+                              size_t groups, uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    if (blockIdx.x == 0) {
+        build_tiles(offsets, E, thr, bm, hdr, fat, thin, nullptr);
+        return;
+    }
+    const size_t i = (size_t)(blockIdx.x - 1) * 1024 + threadIdx.x;     // chunk of 8 values
+    if (i < groups * 16) fp8_quant_chunk(x, i, codes, scales);          // whole groups together
 }
 
 template <int PHASE>
@@ -1429,6 +1449,14 @@ FfnPlanPtrs ffn_plan_ptrs(int T, int E, int k, int H, int I, int wfmt, void* ffn
 hipError_t launch_ffn_plan(const FfnLaunch& a, hipStream_t s) {
     const FfnLayout L = ffn_layout(a.T, a.E, a.k, a.H, a.I, a.wfmt);
     char* ws = reinterpret_cast<char*>(a.ws);
+    if (a.plan_x) {
+        const size_t groups = (size_t)a.T * (a.H / FP8_BLOCK);
+        build_tiles_quant_kernel<<<(unsigned)(1 + (groups * 16 + 1023) / 1024), 1024, 0, s>>>(
+            a.offsets, a.E, a.fat_threshold, fat_bm(a.wfmt), reinterpret_cast<FfnHeader*>(ws + L.hdr),
+            reinterpret_cast<MTile*>(ws + L.fat), reinterpret_cast<MTile*>(ws + L.thin), a.x, groups,
+            reinterpret_cast<uint8_t*>(ws + L.xq), reinterpret_cast<float*>(ws + L.xs));
+        return hipGetLastError();
+    }
     build_tiles_kernel<<<1, 1024, 0, s>>>(a.offsets, a.E, a.fat_threshold, fat_bm(a.wfmt),
                                           reinterpret_cast<FfnHeader*>(ws + L.hdr),
                                           reinterpret_cast<MTile*>(ws + L.fat),
@@ -1441,7 +1469,7 @@ hipError_t launch_ffn_phase(const FfnLaunch& a, int phase, hipStream_t s) {
     hipError_t err = dev_info(d);
     if (err != hipSuccess) return err;
     const bool fat = a.T >= a.fat_threshold;
-    if (a.wfmt == 4) return launch_fp8_phase(make_fp8_args(a), phase, d.cus, fat, s);
+    if (a.wfmt == 4) return launch_fp8_phase(make_fp8_args(a), phase, d.cus, fat, a.plan_x, s);
     const FfnArgs fa = make_args(a);
     // formats 0 and 2 (bf16, plain or row-pair layout) share the kernels
     if (phase == 1) return a.wfmt != 1 ? launch_phase_t<1, 0>(fa, d, fat, s) : launch_phase_t<1, 1>(fa, d, fat, s);

@@ -79,6 +79,35 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
     return (uint32_t)v;
 }
 
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float r) {
+    return make_uint2(fp8_pack4(f[0] * r, f[1] * r, f[2] * r, f[3] * r),
+                      fp8_pack4(f[4] * r, f[5] * r, f[6] * r, f[7] * r));
+}
+
+// Chunk i of 8 values of rows of 128-column groups: 16 consecutive lanes hold
+// a group, and find its scale by four exchanges.
+__device__ __forceinline__ void fp8_quant_chunk(const uint16_t* __restrict__ src, size_t i,
+                                                uint8_t* __restrict__ codes, float* __restrict__ scales) {
+    float f[8];
+    unpack8(ldg16(src + i * 8), f);
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(f[j]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    const float s = fp8_scale(top);
+    *reinterpret_cast<uint2*>(codes + i * 8) = codes8(f, pow2_rcp(s));
+    if ((i & 15) == 0) scales[i >> 4] = s;
+}
+
 struct Fp8Args {
     const uint16_t* x;                  // bf16 [T, H]
     const uint8_t* wg;                  // e4m3 [E, I, H]
@@ -106,8 +135,9 @@ hipError_t launch_quantize_fp8(const uint16_t* src, int64_t mats, int rows, int 
                                float* scales, hipStream_t s);
 
 // One phase of the grouped FFN on e4m3 weights (fp8_ffn.hip): 1 = gate/up
-// (quantises x first), 2 = down.  `fat` false: no route list can be fat.
-hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipStream_t s);
+// (quantises x first unless `x_ready`), 2 = down.  `fat` false: no route list
+// can be fat.
+hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, bool x_ready, hipStream_t s);
 
 // ... over the MFMA M-tiles only (fp8_fat.hip)
 hipError_t launch_fp8_fat_phase(const Fp8Args& a, int phase, int cus, hipStream_t s);

@@ -246,8 +246,8 @@ void ffn_fp8_stream_kernel(Fp8Args a) {
 
 }  // namespace
 
-hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, hipStream_t s) {
-    if (phase == 1) {
+hipError_t launch_fp8_phase(const Fp8Args& a, int phase, int cus, bool fat, bool x_ready, hipStream_t s) {
+    if (phase == 1 && !x_ready) {
         const hipError_t err = launch_quantize_fp8(a.x, 1, a.T, a.H, 1, a.xq, a.xs, s);
         if (err != hipSuccess) return err;
     }

@@ -18,34 +18,12 @@ namespace {
 
 constexpr int QR_THREADS = 256;
 
-__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(v[i] << 16);
-        f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    }
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float r) {
-    return make_uint2(fp8_pack4(f[0] * r, f[1] * r, f[2] * r, f[3] * r),
-                      fp8_pack4(f[4] * r, f[5] * r, f[6] * r, f[7] * r));
-}
-
 __global__ __launch_bounds__(QR_THREADS)
 void fp8_quant_rows_kernel(const uint16_t* __restrict__ src, size_t groups, uint8_t* __restrict__ codes,
                            float* __restrict__ scales) {
     const size_t i = (size_t)blockIdx.x * QR_THREADS + threadIdx.x;     // chunk of 8 values
     if (i >= groups * 16) return;                                       // whole groups leave together
-    float f[8];
-    unpack8(ldg16(src + i * 8), f);
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(f[j]));
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    const float s = fp8_scale(top);
-    *reinterpret_cast<uint2*>(codes + i * 8) = codes8(f, pow2_rcp(s));
-    if ((i & 15) == 0) scales[i >> 4] = s;
+    fp8_quant_chunk(src, i, codes, scales);
 }
 
 __global__ __launch_bounds__(256)

@@ -39,6 +39,7 @@ struct FfnLaunch {
     uint16_t* y;
     void* ws;                       // FFN part of the workspace
     int32_t* counts;                // plan only: per-expert row counts written too (nullable)
+    bool plan_x = false;            // e4m3: the plan's launch quantises x too, not phase 1
 };
 
 size_t ffn_ws_bytes(int T, int E, int k, int H, int I, int wfmt);
