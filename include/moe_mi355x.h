@@ -232,8 +232,8 @@ moe_status moe_grouped_ffn(const uint16_t* x, int wfmt,
  * 128 x 128 block: s_gate, s_up [E, I/128, H/128], s_down [E, H/128, I/128];
  * weight = code * scale (any finite scales; moe_quantize_fp8 with block_rows
  * = 128 makes them).  The activations are quantised as moe_quantize_fp8 with
- * block_rows = 1 does: x by moe_ffn_gate_up on its way in, a = silu(g) * u
- * (fp32) in its epilogue:
+ * block_rows = 1 does: x by moe_ffn_gate_up on its way in (by the whole calls
+ * with the plan), a = silu(g) * u (fp32) in its epilogue:
  *     g[n] = sum_b sx[t, b] s_gate[n/128, b] sum_{h in b} xq[t, h] w_gate[n, h]
  * and likewise u, and y from the codes of a and w_down.  Each 128-column
  * product takes both scales before it is added in fp32.  Short route lists

@@ -130,6 +130,41 @@ def test_two_streams_at_once():
                 assert torch.equal(a, c), i
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 6, 2), (37, 6, 2), (300, 5, 3)])
+def test_captured_whole_call_replays(T, E, k):
+    """moe_grouped_ffn in a graph, on other inputs at each replay, against its phases one by one."""
+    _cuda()
+    H, I = 256, 384
+    dw = F8.dev_weights(F8.make_case(T, E, k, H, I, 77)[2])
+    w = (dw["gate"], dw["up"], dw["down"])
+    kw = dict(s_gate=dw["gate_scale"], s_up=dw["up_scale"], s_down=dw["down_scale"], wfmt=FP8)
+    b = moe.MoELayerBuffers(T, E, k, H, I, FP8)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    off, sp = torch.zeros_like(b.expert_offsets), torch.zeros_like(b.sorted_pair)
+    y, ws = torch.empty_like(b.y_sorted), torch.full_like(b.workspace, 0xFF)
+    graph = None
+    for seed in range(4):
+        logits, xs, _ = F8.make_case(T, E, k, H, I, 200 + seed, 1 + seed if seed + 1 >= k else None)
+        x.copy_(xs)
+        b.workspace.fill_(0xFF)
+        b.forward(torch.from_numpy(logits).cuda(), x, dw)
+        off.copy_(b.expert_offsets)
+        sp.copy_(b.sorted_pair)
+        torch.cuda.synchronize()
+        if graph is None:
+            moe.moe_grouped_ffn(x, *w, off, sp, k, y, ws, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(y, b.y_sorted)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                moe.moe_grouped_ffn(x, *w, off, sp, k, y, ws, **kw)
+        for _ in range(2):
+            y.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, b.y_sorted), seed
+
+
 @pytest.mark.parametrize("T,E,k,G,mask_kind", [(40002, 20, 2, 6, "some"), (30000, 70, 4, 7500, None),
                                                (5000, 8, 2, 5000, "some")])
 def test_many_tokens_and_many_groups(T, E, k, G, mask_kind):
