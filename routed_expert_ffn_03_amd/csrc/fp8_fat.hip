@@ -502,10 +502,12 @@ void ffn_fp8_fat_kernel(Fp8Args a) {
 
 // The row scales of x in sorted order, block-major: xst[b, i] = xs[sorted_pair[i] / k, b].
 // The MFMA-tile kernel then reads the 32 rows of a tile as one line per block.
+// Nothing to do where no list became an M-tile.
 __global__ __launch_bounds__(256)
-void fp8_sort_scales_kernel(const float* __restrict__ xs, const int32_t* __restrict__ sorted_pair, int P, int k, int KB,
-                            float* __restrict__ xst) {
+void fp8_sort_scales_kernel(const FfnHeader* __restrict__ hdr, const float* __restrict__ xs,
+                            const int32_t* __restrict__ sorted_pair, int P, int k, int KB, float* __restrict__ xst) {
     __shared__ float tile[64][33];
+    if (hdr->n_fat == 0) return;
     const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5;           // 8 rows of 32 blocks
     const int l = threadIdx.x & 63, b0 = threadIdx.x >> 6;           // 4 blocks of 64 rows
     for (int base = blockIdx.x * 64; base < P; base += gridDim.x * 64) {
@@ -551,7 +553,7 @@ hipError_t launch_fp8_fat_phase(const Fp8Args& a, int phase, int cus, hipStream_
     if (phase == 1) {
         const int P = a.T * a.k;
         const unsigned blocks = (unsigned)std::min((P - 1) / 64 + 1, 8 * cus);
-        fp8_sort_scales_kernel<<<blocks, 256, 0, s>>>(a.xs, a.sorted_pair, P, a.k, a.H / FP8_BLOCK, a.xst);
+        fp8_sort_scales_kernel<<<blocks, 256, 0, s>>>(a.hdr, a.xs, a.sorted_pair, P, a.k, a.H / FP8_BLOCK, a.xst);
         ffn_fp8_fat_kernel<1><<<cus, FF_THREADS, FF_LDS, s>>>(a);
     } else {
         ffn_fp8_fat_kernel<2><<<cus, FF_THREADS, FF_LDS, s>>>(a);
